@@ -66,6 +66,10 @@ typedef enum pa_status {
 #define PA_DEVERR_SEQ_LEN 0x4      /* seq_len beyond max_blocks_per_seq*block_size */
 #define PA_DEVERR_WAIT_TIMEOUT 0x8 /* a pipeline wait ran out of its time limit */
 #define PA_DEVERR_COPY_PAIR 0x10   /* copy_blocks pair outside the pool */
+#define PA_DEVERR_NO_BLOCKS 0x20   /* plan_append: not enough free blocks, nothing was changed */
+#define PA_DEVERR_PLAN 0x40        /* plan_append: state or counts out of range, nothing was changed */
+#define PA_DEVERR_TREE 0x80        /* a tree length or accepted path out of range */
+#define PA_DEVERR_POSITION 0x100   /* a position beyond the rotation table */
 
 /* Library version, major*10000 + minor*100 + patch. */
 int pa_version(void);
@@ -346,6 +350,196 @@ int pa_decode_contiguous(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_cache
                          const int32_t* seq_lens, int batch, int num_q_heads, int num_kv_heads,
                          int head_dim, int max_len, float scale, void* workspace,
                          size_t workspace_bytes, int variant, void* stream);
+
+/* ==========================================================================
+ * Tree speculation: the device half of a serving step that verifies a tree
+ * of drafted tokens per request.  In the order of a step:
+ *   pa_plan_append          blocks, slots and positions for the drafted tokens
+ *   pa_norm_rope_and_cache  their queries and keys normed and rotated, keys
+ *                           and values written into the slots
+ *   pa_decode_tree          every node attends to its ancestors and the prefix
+ *   pa_tree_accept          the accepted path's rows move behind the prefix
+ * None of them needs the host between two steps: all state (tables, lengths,
+ * free blocks) is in device memory, and a step can be captured into a graph.
+ * ========================================================================== */
+
+/* --------------------------------------------------------------------------
+ * pa_plan_append -- block tables and slot maps on the GPU, from request
+ * lengths.
+ *
+ * The allocator's append for requests that own their blocks ("Paged
+ * attention in LLMs", "The fix: stop demanding one continuous run", "Keeping
+ * track: the block table"), with the free list as a stack in device memory.
+ * Request b has length L = seq_lens[b], holds h = blocks_held[b] blocks (the
+ * first h entries of its table row) and gets c = new_tokens[b] tokens:
+ *
+ *   c < 0 : the request ends: its h blocks go back, length and holding
+ *           become 0.  Its table row is left as it was.
+ *   c >= 0: need = max(0, ceil((L + c) / block_size) - h) blocks are taken
+ *           into table entries h .. h + need - 1.
+ *
+ * Policy, the same as the host allocator's: first all ended requests push
+ * their blocks on the stack (requests in order, blocks in table order), then
+ * the appending requests pop theirs, in order.  The stack is free_blocks[0 ..
+ * num_free[0]), its top last.  Token t of request b has position p = L + t,
+ * slot = table[p / bs] * bs + p % bs; positions[] receives p, or L +
+ * depths[b * depths_stride + t] when depths is given (siblings in a tree share a rotation position).
+ * A request may hold more blocks than its length needs: rejected tokens
+ * leave it so, and the next append uses them.  Sharing (pa_alloc_fork) is
+ * the host allocator's; a pool managed here has one owner per block.
+ *
+ * All or nothing.  When the free blocks do not suffice (PA_DEVERR_NO_BLOCKS)
+ * or an input is out of range (PA_DEVERR_PLAN: L < 0, h outside [0,
+ * max_blocks_per_seq], L + c beyond the table row, c > max_new_tokens, more
+ * tokens than num_slots, num_free or the stack with the returned blocks
+ * outside [0, num_blocks]) nothing is taken or returned: the outputs repeat
+ * the inputs and every slot and position is -1, so that the calls after it
+ * write nothing.
+ *
+ * slot_mapping, positions : device int64 / int32, one entry per token, in one
+ *                of two layouts.  max_new_tokens > 0: padded [batch]
+ *                [max_new_tokens] (num_slots = batch * max_new_tokens).
+ *                max_new_tokens == 0: packed [num_slots], request b's tokens
+ *                from token_starts[b] on.  Entries that belong to no token
+ *                are -1.
+ * token_starts : device int32 [batch + 1], exclusive sums of the counts; may
+ *                be NULL in the padded layout.
+ * *_out        : the state after the call; each may be the input itself.
+ *                Calling again with the same inputs (and not in place) gives
+ *                the same result.
+ * block_tables : device int32 [batch][max_blocks_per_seq], new entries
+ *                written in place.
+ * free_blocks  : device int32 [num_blocks], returned blocks written in place.
+ * appended_out : device int32 [batch] or NULL: max(c, 0), or 0 when the call was
+ *                refused: the tree_lens of the calls that follow.
+ * status_out   : device int32 [1] or NULL: 0, or PA_DEVERR_NO_BLOCKS or
+ *                PA_DEVERR_PLAN when the call was refused.
+ * depths       : device int32 [batch][depths_stride], or with stride 0 one
+ *                row shared by all requests; NULL for a chain.  Padded
+ *                layout only.
+ * batch <= 1048576, num_slots <= 2^30, max_blocks_per_seq * block_size <= 2^31 - 1.
+ * ------------------------------------------------------------------------ */
+int pa_plan_append(int32_t* block_tables, const int32_t* blocks_held, int32_t* free_blocks,
+                   const int32_t* num_free, const int32_t* seq_lens, const int32_t* new_tokens,
+                   const int32_t* depths, int depths_stride, int64_t* slot_mapping,
+                   int32_t* positions, int32_t* token_starts, int32_t* seq_lens_out,
+                   int32_t* blocks_held_out, int32_t* num_free_out, int32_t* appended_out,
+                   int32_t* status_out, int batch, int max_new_tokens, int num_slots, int num_blocks, int block_size,
+                   int max_blocks_per_seq, void* stream);
+
+/* --------------------------------------------------------------------------
+ * pa_norm_rope_and_cache -- per-head norms and rotation of queries and keys,
+ * and the cache write, in one pass.
+ *
+ * For every token t and head, in fp32 and rounded to bf16 once at the end:
+ *
+ *   y = x * rsqrt(mean(x^2) + eps) * weight       (q_weight, k_weight; NULL: y = x)
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
+ *
+ * for the pairs of the first rotary_dim elements: (i, i + rotary_dim / 2), or
+ * (2i, 2i + 1) when interleaved; the others stay.  The angles are row
+ * positions[t] of cos_sin: rotary_dim / 2 cosines, then as many sines.
+ * Queries go to q_out, keys to k_out and / or the pool, values to the pool as
+ * they are, both at slot_mapping[t] as in pa_reshape_and_cache.
+ *
+ * q, k, v      : device bf16; token t's heads [heads][head_dim] lie together
+ *                at t * q_stride (k_stride, v_stride) elements, a multiple of
+ *                8: slices of a fused projection's output need no copy.
+ * q_out        : device bf16 at q_out_stride; may be q itself (same stride).
+ * k_out        : device bf16 at k_out_stride, may be k itself; or NULL.
+ * kv_pool      : device bf16 pool (layout above); NULL: nothing is cached (v
+ *                and slot_mapping are not read).
+ * q_weight, k_weight : device bf16 [head_dim] or NULL.
+ * cos_sin      : device fp32 [max_position][rotary_dim]; NULL with rotary_dim 0.
+ * positions    : device int32 [num_tokens]; NULL with rotary_dim 0.  A
+ *                negative position is padding: q_out and k_out rows become 0,
+ *                nothing is cached.  One >= max_position flags
+ *                PA_DEVERR_POSITION and counts as padding.
+ * slot_mapping : device int64 [num_tokens]; negative: not cached.  One
+ *                beyond the pool flags PA_DEVERR_SLOT and is skipped.
+ * head_dim in {64, 128}; rotary_dim a multiple of 16 up to head_dim, or 0.
+ * num_q_heads or num_kv_heads may be 0 (then those pointers are not read).
+ * ------------------------------------------------------------------------ */
+int pa_norm_rope_and_cache(pa_bf16* q_out, int64_t q_out_stride, pa_bf16* k_out,
+                           int64_t k_out_stride, pa_bf16* kv_pool, const pa_bf16* q,
+                           int64_t q_stride, const pa_bf16* k, int64_t k_stride, const pa_bf16* v,
+                           int64_t v_stride, const pa_bf16* q_weight, const pa_bf16* k_weight,
+                           float eps, const float* cos_sin, int max_position, int rotary_dim,
+                           int interleaved, const int32_t* positions, const int64_t* slot_mapping,
+                           int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                           int num_blocks, int block_size, void* stream);
+
+/* --------------------------------------------------------------------------
+ * pa_decode_tree -- attention of a tree of drafted tokens over the cache.
+ *
+ * pa_decode for the n = tree_lens[b] newest tokens of each request at once,
+ * where the n tokens form a tree rather than a chain: node t (its keys and
+ * values at position L - n + t, L = seq_lens[b]) attends to the committed
+ * prefix [0, L - n) and to the nodes whose bit is set in its row of
+ * tree_mask (its ancestors and itself, or any other set):
+ *
+ *   out[b][t][j] = softmax over the attended positions of
+ *                  (scale * q[b][t][j] . K[pos][h]) times V[pos][h]
+ *
+ * A node that attends to nothing, and every row t >= n, gets out = 0.
+ * What lies at positions that a node does not attend to has no effect on it,
+ * infinities and NaN included.  fp32 online softmax; probabilities are
+ * rounded to bf16 for the tensor-core product, as in pa_decode.
+ *
+ * q, out     : bf16 [batch][num_nodes][num_q_heads][head_dim]; out in device
+ *              or pinned host memory as for pa_decode
+ * tree_mask  : device uint32 rows of ceil(num_nodes / 32) words, bit i % 32
+ *              of word i / 32 = node i; [batch][num_nodes][words], or with
+ *              mask_per_request == 0 one tree [num_nodes][words] for all.
+ *              Bits >= n are ignored.
+ * tree_lens  : device int32 [batch], or NULL: num_nodes for every request.
+ *              One outside [0, min(num_nodes, L)] flags PA_DEVERR_TREE and
+ *              the request's out is 0 (a request with L = 0 is empty and
+ *              never flagged for that).
+ * Other arguments, length and block checks as pa_decode; seq_lens include
+ * the nodes.  num_nodes 1..1024, head_dim in {64, 128}, block_size in
+ * {16, 32}, num_q_heads / num_kv_heads 1..64, batch <= 32768.
+ * workspace from pa_decode_tree_workspace_size (256-byte aligned, no
+ * initialisation; calls that can overlap need one each).
+ * ------------------------------------------------------------------------ */
+int pa_decode_tree_workspace_size(int batch, int num_nodes, int num_q_heads, int num_kv_heads,
+                                  int head_dim, int block_size, int max_seq_len, size_t* bytes_out);
+
+int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool,
+                   const uint32_t* tree_mask, int mask_per_request, const int32_t* block_tables,
+                   const int32_t* seq_lens, const int32_t* tree_lens, int batch, int num_nodes,
+                   int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                   int max_blocks_per_seq, int max_seq_len, float scale, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------------------------------
+ * pa_tree_accept -- keep one path of each request's tree.
+ *
+ * With base = seq_lens[b] - tree_lens[b] the first position of the tree, a =
+ * accept_lens[b] accepted nodes and their indices path[b][0 .. a) in strictly
+ * increasing order (parents come before children):
+ *
+ *   rows of position base + i  <-  rows of position base + path[b][i], i < a
+ *   seq_lens_out[b] = base + a
+ *
+ * keys and values of every head, through the block table, bit for bit.  A
+ * layer's pool is moved by one call; seq_lens_out may be seq_lens itself in
+ * the last layer's call, or NULL.  A length, count or path out of range (L
+ * beyond the table row, n outside [0, min(num_nodes, L)], a outside [0,
+ * min(n, max_path)], an index not above the one before it or >= n) flags
+ * PA_DEVERR_TREE, a block outside the pool PA_DEVERR_BLOCK_ID: then nothing of
+ * that request moves and seq_lens_out[b] = seq_lens[b].  A request with L = 0
+ * is empty: nothing moves, nothing is flagged, seq_lens_out[b] = 0.
+ *
+ * path       : device int32 [batch][max_path]; entries from a on are not read
+ * tree_lens  : device int32 [batch], or NULL: num_nodes for every request
+ * head_dim a multiple of 8; max_path 0..1024.
+ * ------------------------------------------------------------------------ */
+int pa_tree_accept(pa_bf16* kv_pool, const int32_t* path, const int32_t* accept_lens,
+                   const int32_t* tree_lens, const int32_t* block_tables, const int32_t* seq_lens,
+                   int32_t* seq_lens_out, int batch, int num_nodes, int max_path, int num_blocks,
+                   int num_kv_heads, int block_size, int head_dim, int max_blocks_per_seq,
+                   void* stream);
 
 /* Self-test of the bounded pipeline wait used by the kernels: one CTA waits
  * on a barrier phase that nothing completes, for at most limit_ns, then

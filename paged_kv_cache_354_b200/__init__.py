@@ -14,6 +14,7 @@ bf16 tensors are ``torch.bfloat16``; shapes follow ``include/pa.h``:
     kv_cache     [batch, 2, num_kv_heads, max_len, head_dim]  (contiguous decode)
     block_tables int32 [batch, max_blocks_per_seq]; seq_lens int32 [batch]
     slot_mapping int64 [num_tokens]; block_pairs int32 [num_pairs, 2]
+    tree_mask    int32 [num_nodes, words] or [batch, num_nodes, words] (bits)
 """
 
 import ctypes
@@ -36,6 +37,10 @@ PA_DEVERR_SLOT = 0x2
 PA_DEVERR_SEQ_LEN = 0x4
 PA_DEVERR_WAIT_TIMEOUT = 0x8
 PA_DEVERR_COPY_PAIR = 0x10
+PA_DEVERR_NO_BLOCKS = 0x20
+PA_DEVERR_PLAN = 0x40
+PA_DEVERR_TREE = 0x80
+PA_DEVERR_POSITION = 0x100
 
 PA_DECODE_AUTO = 0
 PA_DECODE_CUDA_CORE = 1
@@ -70,6 +75,12 @@ _SIGNATURES = {
                              _P]),
     "pa_decode_contiguous_workspace_size": (_I, [_I, _I, _I, _I, _I, _P]),
     "pa_decode_contiguous": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _c.c_float, _P, _SZ, _I, _P]),
+    "pa_plan_append": (_I, [_P] * 7 + [_I] + [_P] * 8 + [_I] * 6 + [_P]),
+    "pa_norm_rope_and_cache": (_I, [_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _c.c_float, _P]
+                               + [_I] * 3 + [_P, _P] + [_I] * 6 + [_P]),
+    "pa_decode_tree_workspace_size": (_I, [_I] * 7 + [_P]),
+    "pa_decode_tree": (_I, [_P, _P, _P, _P, _I, _P, _P, _P] + [_I] * 9 + [_c.c_float, _P, _SZ, _P]),
+    "pa_tree_accept": (_I, [_P] * 7 + [_I] * 8 + [_P]),
     "pa_selftest_wait_timeout": (_I, [_I64, _P]),
     "pa_alloc_create": (_I, [_I, _I, _P, _P]),
     "pa_alloc_destroy": (_I, [_P]),
@@ -330,6 +341,220 @@ def pa_decode_append(out, q, kv_pool, key, value, slot_mapping, block_tables, se
                                 _ptr(block_tables), _ptr(seq_lens), b, hq, hkv, d, bs, nb, block_tables.shape[1],
                                 int(max_seq_len), float(scale), ws_ptr, ws_bytes, _stream(stream)),
            "pa_decode_append")
+
+
+# --------------------------------------------------------------------------
+# tree speculation
+# --------------------------------------------------------------------------
+def _on_one_device(where, *tensors):
+    """The CUDA device all tensors (None skipped) are on."""
+    device = None
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            if device is None:
+                device = t.device
+            elif t.device != device:
+                raise ValueError(f"{where}: tensors on {device} and {t.device}")
+    return device
+
+
+def _launch(where, device, stream, fn, *args):
+    """Call fn(*args, stream) with ``device`` current."""
+    import torch
+
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, stream.cuda_stream), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream.cuda_stream), where)
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def pa_plan_append(block_tables, blocks_held, free_blocks, num_free, seq_lens, new_tokens, slot_mapping, positions,
+                   block_size, depths=None, token_starts=None, seq_lens_out=None, blocks_held_out=None,
+                   num_free_out=None, appended_out=None, status_out=None, stream=None):
+    """Blocks, slots and positions of every request's new tokens, on the GPU.
+
+    ``slot_mapping`` / ``positions`` are [batch, max_new_tokens] (padded) or
+    1-d (packed; needs ``token_starts`` [batch + 1]).  The state is updated in
+    place unless ``seq_lens_out`` / ``blocks_held_out`` / ``num_free_out`` say
+    otherwise.  ``depths``: int32 [batch, max_new_tokens], or
+    [max_new_tokens] for one tree shared by all requests."""
+    import torch
+
+    where = "pa_plan_append"
+    seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    blocks_held_out = blocks_held if blocks_held_out is None else blocks_held_out
+    num_free_out = num_free if num_free_out is None else num_free_out
+    i32 = torch.int32
+    for t, name in ((block_tables, "block_tables"), (blocks_held, "blocks_held"), (free_blocks, "free_blocks"),
+                    (num_free, "num_free"), (seq_lens, "seq_lens"), (new_tokens, "new_tokens"),
+                    (positions, "positions"), (seq_lens_out, "seq_lens_out"), (blocks_held_out, "blocks_held_out"),
+                    (num_free_out, "num_free_out"), (depths, "depths"), (token_starts, "token_starts"),
+                    (appended_out, "appended_out"), (status_out, "status_out")):
+        if t is not None:
+            _require(t, i32, name)
+    _require(slot_mapping, torch.int64, "slot_mapping")
+    device = _on_one_device(where, block_tables, blocks_held, free_blocks, num_free, seq_lens, new_tokens, positions,
+                            slot_mapping, seq_lens_out, blocks_held_out, num_free_out, depths, token_starts, appended_out,
+                            status_out)
+    b, width = block_tables.shape
+    per_request = (b,)
+    padded = slot_mapping.dim() == 2
+    if (blocks_held.shape != per_request or seq_lens.shape != per_request or new_tokens.shape != per_request
+            or seq_lens_out.shape != per_request or blocks_held_out.shape != per_request or num_free.numel() != 1
+            or num_free_out.numel() != 1 or free_blocks.dim() != 1 or positions.shape != slot_mapping.shape
+            or (padded and slot_mapping.shape[0] != b) or slot_mapping.dim() not in (1, 2)
+            or (token_starts is not None and token_starts.shape != (b + 1,))
+            or (appended_out is not None and appended_out.shape != per_request)
+            or (status_out is not None and status_out.numel() != 1)):
+        raise ValueError(f"{where}: shape mismatch")
+    most = slot_mapping.shape[1] if padded else 0
+    if padded and most == 0:
+        raise ValueError(f"{where}: the padded layout needs at least one column")
+    stride = 0
+    if depths is not None:
+        if not padded or depths.shape not in ((most,), (b, most)):
+            raise ValueError(f"{where}: shape mismatch")
+        stride = most if depths.dim() == 2 else 0
+    _launch(where, device, stream, lib.pa_plan_append, _adr(block_tables), _adr(blocks_held), _adr(free_blocks),
+            _adr(num_free), _adr(seq_lens), _adr(new_tokens), _adr(depths), stride, _adr(slot_mapping),
+            _adr(positions), _adr(token_starts), _adr(seq_lens_out), _adr(blocks_held_out), _adr(num_free_out),
+            _adr(appended_out), _adr(status_out), b, most, slot_mapping.numel(), free_blocks.shape[0], int(block_size), width)
+
+
+def _token_rows(t, dtype, name):
+    """Token stride of a [tokens, heads, head_dim] tensor whose heads lie together."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if n and h and ((d > 1 and s2 != 1) or (h > 1 and s1 != d)):
+        raise ValueError(f"{name}: a token's heads must lie together")
+    return s0 if n > 1 else h * d
+
+
+def pa_norm_rope_and_cache(q_out, q, k, v, kv_pool, slot_mapping, positions, cos_sin, q_weight=None, k_weight=None,
+                           eps=1e-6, interleaved=False, k_out=None, stream=None):
+    """Norm and rotate queries and keys; queries go to ``q_out`` (may be ``q``),
+    keys and values into ``kv_pool`` at ``slot_mapping`` (and / or keys to
+    ``k_out``).  q, k, v are [tokens, heads, head_dim], strided by token;
+    ``cos_sin`` fp32 [max_position, rotary_dim] (None: no rotation)."""
+    import torch
+
+    where = "pa_norm_rope_and_cache"
+    bf16 = torch.bfloat16
+    qs, qos, ks = _token_rows(q, bf16, "q"), _token_rows(q_out, bf16, "q_out"), _token_rows(k, bf16, "k")
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    vs = kos = 0
+    blocks = block_size = 0
+    if q_out.shape != q.shape or k.shape != (n, hkv, d):
+        raise ValueError(f"{where}: shape mismatch")
+    if kv_pool is not None:
+        _require(kv_pool, bf16, "kv_pool")
+        _require(slot_mapping, torch.int64, "slot_mapping")
+        vs = _token_rows(v, bf16, "v")
+        blocks, two, pool_heads, block_size, pool_dim = kv_pool.shape
+        if v.shape != k.shape or slot_mapping.numel() != n or (two, pool_heads, pool_dim) != (2, hkv, d):
+            raise ValueError(f"{where}: shape mismatch")
+    if k_out is not None:
+        kos = _token_rows(k_out, bf16, "k_out")
+        if k_out.shape != k.shape:
+            raise ValueError(f"{where}: shape mismatch")
+    most = rotary = 0
+    if cos_sin is not None:
+        _require(cos_sin, torch.float32, "cos_sin")
+        most, rotary = cos_sin.shape
+    if positions is not None:
+        _require(positions, torch.int32, "positions")
+        if positions.numel() != n:
+            raise ValueError(f"{where}: shape mismatch")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _require(w, bf16, name)
+            if w.shape != (d,):
+                raise ValueError(f"{where}: shape mismatch")
+    device = _on_one_device(where, q, q_out, k, k_out, v if kv_pool is not None else None, kv_pool,
+                            slot_mapping if kv_pool is not None else None, positions, cos_sin, q_weight, k_weight)
+    _launch(where, device, stream, lib.pa_norm_rope_and_cache, _adr(q_out), qos, _adr(k_out), kos, _adr(kv_pool),
+            _adr(q), qs, _adr(k), ks, _adr(v) if kv_pool is not None else None, vs, _adr(q_weight), _adr(k_weight),
+            float(eps), _adr(cos_sin), most, rotary, 1 if interleaved else 0, _adr(positions),
+            _adr(slot_mapping) if kv_pool is not None else None, n, hq, hkv, d, blocks, block_size)
+
+
+def pa_decode_tree_workspace_size(batch, num_nodes, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len):
+    nbytes = ctypes.c_size_t(0)
+    _check(lib.pa_decode_tree_workspace_size(batch, num_nodes, num_q_heads, num_kv_heads, head_dim, block_size,
+                                             max_seq_len, ctypes.byref(nbytes)), "pa_decode_tree_workspace_size")
+    return nbytes.value
+
+
+def pa_decode_tree(out, q, kv_pool, tree_mask, block_tables, seq_lens, max_seq_len, scale, workspace, tree_lens=None,
+                   stream=None):
+    """Attention of a tree of drafted tokens per request: q, out bf16
+    [B, T, Hq, D]; ``tree_mask`` int32 bits [T, ceil(T/32)] (one tree for all)
+    or [B, T, ceil(T/32)]; ``tree_lens`` int32 [B] (None: T each)."""
+    import torch
+
+    where = "pa_decode_tree"
+    _require(out, torch.bfloat16, "out", pinned_ok=True)
+    _require(q, torch.bfloat16, "q")
+    _require(kv_pool, torch.bfloat16, "kv_pool")
+    _require(tree_mask, torch.int32, "tree_mask")
+    _require(block_tables, torch.int32, "block_tables")
+    _require(seq_lens, torch.int32, "seq_lens")
+    _require(workspace, torch.uint8, "workspace")
+    if tree_lens is not None:
+        _require(tree_lens, torch.int32, "tree_lens")
+    nb, two, hkv, bs, d = kv_pool.shape
+    b, t, hq, dq = q.shape
+    rows = (t, (t + 31) // 32)
+    if (out.shape != q.shape or dq != d or two != 2 or block_tables.dim() != 2 or block_tables.shape[0] != b
+            or seq_lens.shape != (b,) or (tree_lens is not None and tree_lens.shape != (b,))
+            or tree_mask.shape not in (rows, (b,) + rows)):
+        raise ValueError(f"{where}: shape mismatch")
+    device = _on_one_device(where, q, out, kv_pool, tree_mask, block_tables, seq_lens, workspace, tree_lens)
+    _launch(where, device, stream, lib.pa_decode_tree, _adr(out), _adr(q), _adr(kv_pool), _adr(tree_mask),
+            1 if tree_mask.dim() == 3 else 0, _adr(block_tables), _adr(seq_lens), _adr(tree_lens), b, t, hq, hkv, d,
+            bs, nb, block_tables.shape[1], int(max_seq_len), float(scale), _adr(workspace), workspace.numel())
+
+
+def pa_tree_accept(kv_pool, path, accept_lens, block_tables, seq_lens, tree_lens, seq_lens_out=None, num_nodes=None,
+                   stream=None):
+    """Move the rows of each request's accepted path (node indices ``path``
+    [B, max_path], the first ``accept_lens[b]`` of them) behind its committed
+    prefix; ``seq_lens_out`` (None: not written; may be ``seq_lens``) receives
+    the new lengths.  ``tree_lens``: int32 [B] nodes per request, or None and
+    ``num_nodes`` for all."""
+    import torch
+
+    where = "pa_tree_accept"
+    _require(kv_pool, torch.bfloat16, "kv_pool")
+    for t, name in ((path, "path"), (accept_lens, "accept_lens"), (block_tables, "block_tables"),
+                    (seq_lens, "seq_lens"), (tree_lens, "tree_lens"), (seq_lens_out, "seq_lens_out")):
+        if t is not None:
+            _require(t, torch.int32, name)
+    nb, two, hkv, bs, d = kv_pool.shape
+    b, most = path.shape
+    if (two != 2 or accept_lens.shape != (b,) or seq_lens.shape != (b,) or block_tables.shape[0] != b
+            or (tree_lens is not None and tree_lens.shape != (b,))
+            or (seq_lens_out is not None and seq_lens_out.shape != (b,))):
+        raise ValueError(f"{where}: shape mismatch")
+    if tree_lens is None and num_nodes is None:
+        raise ValueError(f"{where}: tree_lens or num_nodes")
+    nodes = 0x7fffffff if num_nodes is None else int(num_nodes)
+    device = _on_one_device(where, kv_pool, path, accept_lens, block_tables, seq_lens, tree_lens, seq_lens_out)
+    _launch(where, device, stream, lib.pa_tree_accept, _adr(kv_pool), _adr(path), _adr(accept_lens), _adr(tree_lens),
+            _adr(block_tables), _adr(seq_lens), _adr(seq_lens_out), b, nodes, most, nb, hkv, bs, d,
+            block_tables.shape[1])
 
 
 def pa_selftest_wait_timeout(limit_ns, stream=None):

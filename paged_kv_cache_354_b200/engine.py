@@ -1,5 +1,9 @@
 """One layer's paged KV cache on one GPU, driven through the C ABI.
 
+``PagedDecodeCache``: one new token per request and step, blocks handed out
+by the host allocator.  ``PagedTreeCache``: a tree of drafted tokens per
+request and step, all state in device memory (see the class).
+
 A decode step of a serving loop, in the order the method needs it:
 
 1. host: the C++ allocator gives every request a slot for its new token,
@@ -21,8 +25,9 @@ import ctypes
 import numpy as np
 import torch
 
-from . import (PA_DECODE_AUTO, PaAlloc, _check, lib, pa_copy_blocks, pa_decode, pa_decode_append,
-               pa_decode_workspace_size, pa_reshape_and_cache)
+from . import (PA_DECODE_AUTO, PaAlloc, _check, lib, pa_copy_blocks, pa_decode, pa_decode_append, pa_decode_tree,
+               pa_decode_tree_workspace_size, pa_decode_workspace_size, pa_norm_rope_and_cache, pa_plan_append,
+               pa_reshape_and_cache, pa_tree_accept)
 
 
 def _align(n, a=256):
@@ -229,3 +234,97 @@ class PagedDecodeCache:
         fused = self.partition_tokens == 0 and self.variant == PA_DECODE_AUTO and self.schedule == "balanced"
         cache_write = 0 if fused else 1
         return (1 if npairs else 0) + cache_write + 1 + (1 if self.num_partitions > 1 else 0)
+
+
+class PagedTreeCache:
+    """One layer's paged cache for speculative decoding with token trees.
+
+    Block tables, lengths, the free blocks and every step's slots live on the
+    GPU, so a step needs nothing from the host and can be captured:
+
+    1. ``step``: blocks, slots and positions for the drafted nodes
+       (``pa_plan_append``), their queries and keys normed, rotated and cached
+       (``pa_norm_rope_and_cache``), every node attended over its request's
+       prefix and its own ancestors (``pa_decode_tree``);
+    2. the caller verifies the drafts and picks a path per request;
+    3. ``accept``: the path's rows move behind the prefix, the lengths follow
+       (``pa_tree_accept``).
+
+    ``prefill`` brings prompts in and ``release`` ends requests.  A step that
+    finds too few free blocks changes nothing: ``status`` is then not 0 and
+    ``appended`` is 0 everywhere, so its outputs are 0 and its ``accept``
+    moves nothing.
+    """
+
+    def __init__(self, num_blocks, num_q_heads, num_kv_heads, head_dim, block_size, max_batch, max_seq_len, max_nodes,
+                 cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, initial_order=None,
+                 device="cuda"):
+        self.hq, self.hkv, self.d, self.bs = num_q_heads, num_kv_heads, head_dim, block_size
+        self.max_batch, self.max_nodes = int(max_batch), int(max_nodes)
+        self.max_blocks = -(-int(max_seq_len) // block_size)
+        self.max_seq_len = self.max_blocks * block_size
+        self.cos_sin, self.q_weight, self.k_weight = cos_sin, q_weight, k_weight
+        self.eps, self.interleaved = eps, interleaved
+        self.device = torch.device(device)
+        self.scale = 1.0 / float(np.sqrt(head_dim))
+
+        def ints(*shape, dtype=torch.int32):
+            return torch.zeros(shape, dtype=dtype, device=self.device)
+
+        self.pool = torch.empty((int(num_blocks), 2, num_kv_heads, block_size, head_dim), dtype=torch.bfloat16,
+                                device=self.device)
+        order = np.arange(num_blocks) if initial_order is None else np.asarray(initial_order)
+        # a stack, its top last: initial_order is the order of the first pops
+        self.free = torch.as_tensor(order[::-1].astype(np.int32)).to(self.device)
+        self.num_free = torch.full((1,), int(num_blocks), dtype=torch.int32, device=self.device)
+        self.tables = ints(self.max_batch, self.max_blocks)
+        self.held, self.lens = ints(self.max_batch), ints(self.max_batch)
+        self.appended, self.status = ints(self.max_batch), ints(1)
+        self.slots = ints(self.max_batch, self.max_nodes, dtype=torch.int64)
+        self.positions = ints(self.max_batch, self.max_nodes)
+        self.starts = ints(self.max_batch + 1)
+        self.q = torch.empty((self.max_batch, self.max_nodes, num_q_heads, head_dim), dtype=torch.bfloat16,
+                             device=self.device)
+        self.workspace = torch.empty(
+            pa_decode_tree_workspace_size(self.max_batch, self.max_nodes, num_q_heads, num_kv_heads, head_dim,
+                                          block_size, self.max_seq_len), dtype=torch.uint8, device=self.device)
+
+    def _append(self, new_tokens, slots, positions, depths=None):
+        pa_plan_append(self.tables, self.held, self.free, self.num_free, self.lens, new_tokens, slots, positions,
+                       self.bs, depths=depths, token_starts=self.starts, appended_out=self.appended,
+                       status_out=self.status)
+
+    def _write(self, q_out, q, k, v, slots, positions):
+        pa_norm_rope_and_cache(q_out, q, k, v, self.pool, slots, positions, self.cos_sin, q_weight=self.q_weight,
+                               k_weight=self.k_weight, eps=self.eps, interleaved=self.interleaved)
+
+    def prefill(self, new_tokens, q, k, v, q_out):
+        """Cache prompts, packed: ``new_tokens`` int32 [max_batch] tokens each,
+        q / k / v [tokens, heads, head_dim] in request order (more rows than
+        tokens: the rest is padding).  ``q_out`` receives the normed and
+        rotated queries; returns the tokens' (slots, positions)."""
+        n = q.shape[0]
+        slots = torch.empty(n, dtype=torch.int64, device=self.device)
+        positions = torch.empty(n, dtype=torch.int32, device=self.device)
+        self._append(new_tokens, slots, positions)
+        self._write(q_out, q, k, v, slots, positions)
+        return slots, positions
+
+    def step(self, q, k, v, new_tokens, tree_mask, depths, out):
+        """One tree per request: q [max_batch * max_nodes, Hq, D], k / v alike
+        with Hkv heads (rows of a padded batch, token stride free);
+        ``new_tokens`` int32 [max_batch] nodes each, ``tree_mask`` and
+        ``depths`` as in pa_decode_tree and pa_plan_append; ``out``
+        [max_batch, max_nodes, Hq, D]."""
+        self._append(new_tokens, self.slots, self.positions, depths)
+        self._write(self.q.view(-1, self.hq, self.d), q, k, v, self.slots, self.positions)
+        pa_decode_tree(out, self.q, self.pool, tree_mask, self.tables, self.lens, self.max_seq_len, self.scale,
+                       self.workspace, tree_lens=self.appended)
+
+    def accept(self, path, accept_lens):
+        """Keep ``path[b][:accept_lens[b]]`` of the last step's nodes."""
+        pa_tree_accept(self.pool, path, accept_lens, self.tables, self.lens, self.appended, seq_lens_out=self.lens)
+
+    def release(self, ended):
+        """End the requests where ``ended`` (bool [max_batch]) is true."""
+        self._append(torch.where(ended, -1, 0).int(), self.slots, self.positions)
