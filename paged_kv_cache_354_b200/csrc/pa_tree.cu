@@ -63,9 +63,10 @@ struct TreeArgs {
   const int32_t* block_tables;
   const int32_t* seq_lens;
   const int32_t* tree_lens;
-  float* part_o;      // [CTAs][2][2 * kRows][D] unnormalised, at the row's kept maximum
+  float4* part_o;     // [CTAs][2][D / 4][2 * kRows] unnormalised, at the row's kept maximum:
+                      // a warp, one row per lane, writes 512 bytes in a row
   float2* part_ml;    // [CTAs][2][2 * kRows] (kept maximum, sum)
-  int* prefix_out;    // [batch + 1] unit prefix sums, per KV head
+  int* prefix_out;    // [batch + 1] units before each request
   int32_t* err;
   int batch, nodes, words, num_q_heads, num_kv_heads, group;
   int tile_tokens;    // tokens per row tile
@@ -74,6 +75,7 @@ struct TreeArgs {
   int extra, min_units;
   float scale_log2;   // |scale| * log2(e)
   int negative;       // scale < 0: logits change sign
+  int wide_out;       // out is 32-byte aligned
 };
 
 // Length and node count of request b after the device checks; n = 0 where
@@ -100,70 +102,57 @@ __device__ __forceinline__ int pairs_of(const TreeArgs& a, int n) {
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
 // CTAs that share `total` units: at least min_units each.
-__device__ __forceinline__ int ctas_for(const TreeArgs& a, long long total, int ctas) {
-  return static_cast<int>(max(1ll, min(static_cast<long long>(ctas), total / max(a.min_units, 1))));
+__device__ __forceinline__ int ctas_for(const TreeArgs& a, int total, int ctas) {
+  return max(1, min(ctas, total / a.min_units));
 }
-__device__ __forceinline__ long long range_begin(long long total, int c, int ctas) { return total * c / ctas; }
-// The CTA whose range holds unit u.
-__device__ __forceinline__ int cta_of(long long total, long long u, int ctas) {
-  return static_cast<int>((static_cast<long long>(ctas) * (u + 1) + total - 1) / total - 1);
+// First unit of CTA c's share, floor(total * c / ctas), without a 64-bit division.
+__device__ __forceinline__ int range_begin(int total, int c, int ctas) {
+  const int q = total / ctas;
+  return q * c + (total - q * ctas) * c / ctas;
+}
+// The CTA whose share holds unit u: one guess, then at most a step or two.
+__device__ __forceinline__ int cta_of(int total, int u, int ctas) {
+  int c = min(ctas - 1, static_cast<int>(static_cast<float>(u) * static_cast<float>(ctas) / static_cast<float>(total)));
+  while (range_begin(total, c, ctas) > u) --c;
+  while (c + 1 < ctas && range_begin(total, c + 1, ctas) <= u) ++c;
+  return c;
 }
 
 // prefix[b] = units per KV head of the requests before b, b in [0, batch].
 template <int BS>
-__device__ __forceinline__ void unit_prefix(int* prefix, int* scan, const TreeArgs& a, bool report) {
-  const int t = threadIdx.x;
-  const int per = (a.batch + kThreads - 1) / kThreads;
-  const int lo = min(a.batch, t * per), hi = min(a.batch, lo + per);
-  int sum = 0;
-  for (int b = lo; b < hi; ++b) {
-    int len, n;
-    tree_lengths<BS>(a, b, report, len, n);
-    const int units = n > 0 ? pairs_of(a, n) * (tiles_of(len) + a.extra) : 0;
-    prefix[b] = units;
-    sum += units;
-  }
-  scan[t] = sum;
-  __syncthreads();
-  if (t < 32) {  // exclusive scan of the kThreads partial sums by one warp
-    constexpr int kPer = kThreads / 32;
-    int run = 0;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) run += scan[t * kPer + e];
-    int incl = run;
+__device__ __forceinline__ void unit_prefix(int* prefix, int* sums, const TreeArgs& a, bool report) {
+  constexpr int kWarps = kThreads / 32;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  int carry = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    const int b = b0 + t;
+    int units = 0;
+    if (b < a.batch) {
+      int len, n;
+      tree_lengths<BS>(a, b, report, len, n);
+      if (n > 0) units = pairs_of(a, n) * (tiles_of(len) + a.extra);
+    }
+    int incl = units;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(kFull, incl, off);
-      if (t >= off) incl += y;
+      if (lane >= off) incl += y;
     }
-    int excl = incl - run;
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int before = carry, all = carry;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int v = scan[t * kPer + e];
-      scan[t * kPer + e] = excl;
-      excl += v;
+    for (int w = 0; w < kWarps; ++w) {
+      const int x = sums[w];
+      before += w < warp ? x : 0;
+      all += x;
     }
-    if (t == 31) prefix[a.batch] = incl;
+    if (b < a.batch) prefix[b] = before + incl - units;
+    carry = all;
+    __syncthreads();
   }
+  if (t == 0) prefix[a.batch] = carry;
   __syncthreads();
-  int run = scan[t];
-  for (int b = lo; b < hi; ++b) {
-    const int units = prefix[b];
-    prefix[b] = run;
-    run += units;
-  }
-  __syncthreads();
-}
-
-// The largest b with hkv * prefix[b] <= u (requests without units are skipped).
-__device__ __forceinline__ int request_of(const int* prefix, int batch, int hkv, long long u) {
-  int lo = 0, hi = batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<long long>(hkv) * prefix[mid] <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
 }
 
 // One CTA's share of one item, published by the producer.
@@ -200,7 +189,7 @@ struct Geo {
   static constexpr int kK = kQ + 2 * kQBytes;
   static constexpr int kV = kK + kKStages * kTileBytes;
   static constexpr int kBar = kV + kVStages * kTileBytes;
-  static constexpr int kNumBars = 2 * kKStages + 3 * kVStages + 2 * 6 + 2 + kSegs;
+  static constexpr int kNumBars = 2 * kKStages + 3 * kVStages + 2 * 7 + 1 + kSegs;
   static constexpr int kSeg = (kBar + 8 * kNumBars + 15) & ~15;
   static constexpr int kXch = kSeg + kSegs * static_cast<int>(sizeof(Segment));  // float2 [2][kRows]
   static constexpr int kMisc = kXch + 2 * kRows * 8;  // tmem base, abort, issued k, v, q loads
@@ -208,8 +197,8 @@ struct Geo {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kS = 0;              // S / P of stream s at kS + 128 s
   static constexpr int kO = 2 * kTile;      // O of stream s at kO + D s
-  // the prefix sums and their scan fit the idle rings at any batch
-  static_assert(4 * (kMaxBatch + 8 + kThreads) <= (kKStages + kVStages) * kTileBytes, "prefix table");
+  // the prefix sums fit the idle rings at any batch
+  static_assert(4 * (kMaxBatch + 1) <= (kKStages + kVStages) * kTileBytes, "prefix table");
   static_assert(kTotal <= 232448, "shared memory per CTA");
 };
 
@@ -219,11 +208,80 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A wait of a whole warp: true when every lane saw the phase complete.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
+
+// Two fp32 operations per instruction.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)), "l"(reinterpret_cast<uint64_t&>(z)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
+  return r;
+}
+
+// Bounded wait for a phase: the clock is read only once the wait has been
+// long, so a short one costs no more than its polls.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 127u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kWaitLimitNs) return false;
+    }
+  }
+  return true;
+}
+// ... of a whole warp: true when every lane saw the phase complete.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  const bool ok = mbar_wait(bar, parity);
+  const bool ok = wait(bar, parity);
   return __all_sync(kFull, ok);
 }
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+// 64 bytes of one row per thread: whole sectors where the alignment allows.
+__device__ __forceinline__ void store_64_bytes(__nv_bfloat16* to, const uint32_t (&w)[16], int wide) {
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * i), "r"(w[i]),
+                   "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                   "r"(w[i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<uint4*>(to + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
+}
+
+// A ring's next stage and the parity of its round.
+template <int N>
+struct Ring {
+  int stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == N) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+};
 
 __device__ __forceinline__ bool not_finite(uint32_t pair) {
   return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;
@@ -270,9 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_full = [&](int s) { return bar(kPairBars + 6 + s); };
   auto pv_done = [&](int s) { return bar(kPairBars + 8 + s); };
   auto xch_full = [&](int s) { return bar(kPairBars + 10 + s); };
-  const uint32_t o_free = bar(kPairBars + 12);
-  const uint32_t drain = bar(kPairBars + 13);
-  auto seg_full = [&](int j) { return bar(kPairBars + 14 + j); };
+  auto o_free = [&](int s) { return bar(kPairBars + 12 + s); };
+  const uint32_t drain = bar(kPairBars + 14);
+  auto seg_full = [&](int j) { return bar(kPairBars + 15 + j); };
   volatile Segment* segs = reinterpret_cast<volatile Segment*>(smem + G::kSeg);
   float2* xch = reinterpret_cast<float2*>(smem + G::kXch);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kMisc);
@@ -290,23 +348,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < VS; ++s) {
       mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 1);
-      mbar_init(v_clean(s), 64);
+      mbar_init(v_empty(s), 3);  // the product and the two cleaning warps
+      mbar_init(v_clean(s), 2);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 1);
       mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), 128);
+      mbar_init(p_full(s), 4);  // one arrival per warp
       mbar_init(pv_done(s), 1);
       mbar_init(xch_full(s), 128);
+      mbar_init(o_free(s), 256);
     }
-    mbar_init(o_free, 256);
     mbar_init(drain, 1);
     for (int j = 0; j < G::kSegs; ++j) mbar_init(seg_full(j), 1);
     *abort_flag = 0;
     issued[0] = issued[1] = issued[2] = 0;
     fence_barrier_init();
+    prefetch_tensor_map(&kv_map);
+    prefetch_tensor_map(&q_map);
   }
   if (warp == 1) {
     __syncwarp();
@@ -318,107 +378,141 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the unit prefix sums, in the still idle rings
   int* prefix = reinterpret_cast<int*>(smem + G::kK);
-  unit_prefix<BS>(prefix, prefix + ((a.batch + 4) & ~3), a, blockIdx.x == 0);
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= a.batch; i += kThreads) a.prefix_out[i] = prefix[i];
+  unit_prefix<BS>(prefix, reinterpret_cast<int*>(smem + G::kXch), a, blockIdx.x == 0);
   const int hkv = a.num_kv_heads;
-  const long long total = static_cast<long long>(hkv) * prefix[a.batch];
+  const int total = hkv * prefix[a.batch];  // fits: checked on the host
   const int ctas = ctas_for(a, total, gridDim.x);
   const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= ctas;
-  const long long u_begin = idle ? 0 : range_begin(total, blockIdx.x, ctas);
-  const long long u_end = idle ? 0 : range_begin(total, blockIdx.x + 1, ctas);
-  const int b_first = idle ? 0 : request_of(prefix, a.batch, hkv, u_begin);
-  const long long r_first = idle ? 0 : u_begin - static_cast<long long>(hkv) * prefix[b_first];
+  const int u_begin = idle ? 0 : range_begin(total, blockIdx.x, ctas);
+  const int u_end = idle ? 0 : range_begin(total, blockIdx.x + 1, ctas);
+  int* found = reinterpret_cast<int*>(smem + G::kXch) + 64;  // the request of the first unit
+  for (int b = threadIdx.x; b < a.batch; b += kThreads) {
+    const int lo = hkv * prefix[b], hi = hkv * prefix[b + 1];
+    if (lo <= u_begin && u_begin < hi) {
+      found[0] = b;
+      found[1] = u_begin - lo;
+    }
+    if (blockIdx.x == 0) a.prefix_out[b] = lo;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix_out[a.batch] = total;
   fence_proxy_async_smem();  // the rings' generic writes above, TMA writes below
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  const int b_first = idle ? 0 : found[0], r_first = idle ? 0 : found[1];
 
   auto give_up = [&]() {
     flag_error(a.err, PA_DEVERR_WAIT_TIMEOUT);
     *abort_flag = 1;
   };
 
+  // a row's 128 logits stay in registers: the softmax warpgroups take the
+  // ones that the other four warps do not need, 88 + 2 * 208 = 3 * 168
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     // walks the CTA's units; real segments are published in a ring of
     // records.  A record is overwritten kSegs segments later: by then at
     // least kSegs - 1 - kVStages >= 4 later segments' products are done, so
     // both warpgroups, which take turns, are past it.
-    if (lane == 0) {
-      prefetch_tensor_map(&kv_map);
-      prefetch_tensor_map(&q_map);
+    struct Item {
+      int b, h, rp, len, n, tiles, pairs;
+    };
+    auto load_request = [&](Item& it) {
+      tree_lengths<BS>(a, it.b, false, it.len, it.n);
+      it.tiles = tiles_of(it.len);
+      it.pairs = pairs_of(a, it.n);
+    };
+    auto next_item = [&](Item it) -> Item {  // units are left, so there is one
+      if (++it.rp == it.pairs) {
+        it.rp = 0;
+        if (++it.h == hkv) {
+          it.h = 0;
+          do {
+            ++it.b;
+            load_request(it);
+          } while (it.n == 0);
+        }
+      }
+      return it;
+    };
+    constexpr int kAhead = 32 / G::kTileBlocks;  // tiles per warp load of table entries
+    auto fetch = [&](const Item& it, int tile) -> int {
+      const int e = tile * G::kTileBlocks + lane;
+      int block = 0;
+      if (e * BS < it.len) {
+        block = __ldg(a.block_tables + static_cast<int64_t>(it.b) * a.max_blocks + e);
+        if (static_cast<unsigned>(block) >= static_cast<unsigned>(a.num_blocks)) {
+          flag_error(a.err, PA_DEVERR_BLOCK_ID);
+          block = a.num_blocks;  // past the tensor map: TMA fills with zeros
+        }
+      }
+      return block;
+    };
+    Item cur{b_first, 0, 0, 0, 0, 0, 0};
+    int k = 0, ahead = 0;
+    if (!idle) {
+      load_request(cur);
+      const int item = r_first / (cur.tiles + a.extra);
+      k = r_first - item * (cur.tiles + a.extra);
+      cur.h = item / cur.pairs;
+      cur.rp = item - cur.h * cur.pairs;
+      ahead = fetch(cur, k);
     }
-    int b = b_first;
-    int len = 0, n = 0;
-    if (!idle) tree_lengths<BS>(a, b, false, len, n);
-    int tiles = tiles_of(len), np = pairs_of(a, n);
-    long long item = idle ? 0 : r_first / (tiles + a.extra);
-    int k = idle ? 0 : static_cast<int>(r_first - item * (tiles + a.extra));
-    int h = np > 0 ? static_cast<int>(item / np) : 0;
-    int rp = np > 0 ? static_cast<int>(item - static_cast<long long>(h) * np) : 0;
-    long long u = u_begin;
+    int u = u_begin;
     int seg = 0, first = 1, kc = 0, vc = 0, qc = 0;
+    Ring<KS> kr;
+    Ring<VS> vr;
     bool ok = true;
     while (u < u_end && ok) {
-      const int span = static_cast<int>(min(static_cast<long long>(tiles + a.extra - k), u_end - u));
-      const int cnt = max(0, min(k + span, tiles) - k);  // real tiles
+      const int span = min(cur.tiles + a.extra - k, u_end - u);
+      const int cnt = max(0, min(k + span, cur.tiles) - k);  // real tiles
+      Item after = cur;
+      int after_entries = 0;
+      if (u + span < u_end) {  // the next item's first table entries, a segment ahead
+        after = next_item(cur);
+        after_entries = fetch(after, 0);
+      }
       if (cnt > 0) {
-        const int token0 = rp * 2 * a.tile_tokens;
-        const bool two = n - token0 > a.tile_tokens;
+        const int token0 = cur.rp * 2 * a.tile_tokens;
+        const bool two = cur.n - token0 > a.tile_tokens;
         if (lane == 0) {
           volatile Segment& s = segs[seg % G::kSegs];
-          s.b = b;
-          s.h = h;
+          s.b = cur.b;
+          s.h = cur.h;
           s.token0 = token0;
-          s.len = len;
-          s.n = n;
+          s.len = cur.len;
+          s.n = cur.n;
           s.tile0 = k;
           s.steps = two ? 2 * cnt : cnt;
-          s.flags = (two ? kTwo : 0) | (k == 0 && cnt == tiles ? kComplete : 0);
+          s.flags = (two ? kTwo : 0) | (k == 0 && cnt == cur.tiles ? kComplete : 0);
           s.slot = first ? 0 : 1;
           s.poison = 0;
           mbar_arrive(seg_full(seg % G::kSegs));  // release: the record is visible
         }
         ++seg;
-        const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.max_blocks;
-        const int blocks = (len + BS - 1) / BS;
-        constexpr int kAhead = 32 / G::kTileBlocks;  // tiles per warp load of table entries
-        int next = 0;
-        auto fetch = [&](int tile) -> int {
-          const int e = tile * G::kTileBlocks + lane;
-          int block = 0;
-          if (e < blocks) {
-            block = __ldg(table + e);
-            if (static_cast<unsigned>(block) >= static_cast<unsigned>(a.num_blocks)) {
-              flag_error(a.err, PA_DEVERR_BLOCK_ID);
-              block = a.num_blocks;  // past the tensor map: TMA fills with zeros
-            }
-          }
-          return block;
-        };
-        next = fetch(k);
+        const int blocks = (cur.len + BS - 1) / BS;
         int entries = 0;
         for (int i = 0; i < cnt && ok; ++i) {
           if (i % kAhead == 0) {
-            entries = next;
-            if (i + kAhead < cnt) next = fetch(k + i + kAhead);
+            entries = ahead;
+            if (i + kAhead < cnt) ahead = fetch(cur, k + i + kAhead);
           }
           const int mine = __shfl_sync(kFull, entries, (i % kAhead) * G::kTileBlocks + lane % G::kTileBlocks);
           const int live = min(G::kTileBlocks, blocks - (k + i) * G::kTileBlocks);  // blocks in the tile
-          const int ks = kc % KS, vs = vc % VS;
-          ok = warp_wait(k_empty(ks), ((kc / KS) & 1) ^ 1);
+          ok = warp_wait(k_empty(kr.stage), kr.parity ^ 1);
           if (!ok) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(k_full(ks), live * G::kBlockBytes);
-            issued[0] = kc + 1;
+            mbar_arrive_expect_tx(k_full(kr.stage), live * G::kBlockBytes);
+            issued[0] = ++kc;
           }
           __syncwarp();
           if (lane < live)
-            tma_load_5d(sbase + G::kK + ks * G::kTileBytes + lane * G::kBlockBytes, &kv_map, k_full(ks), 0, 0, 0,
-                        h * (BS / 8), 2 * mine);
-          ++kc;
+            tma_load_5d(sbase + G::kK + kr.stage * G::kTileBytes + lane * G::kBlockBytes, &kv_map, k_full(kr.stage), 0,
+                        0, 0, cur.h * (BS / 8), 2 * mine);
+          kr.next();
           // the queries, after the first keys: their buffer may still be in use
           for (int j = 0; i == 0 && j < (two ? 2 : 1) && ok; ++j) {
             const int qs = qc & 1;
@@ -430,39 +524,29 @@ __global__ void __launch_bounds__(kThreads, 1)
               issued[2] = qc;
 #pragma unroll
               for (int x = 0; x < G::kSlabs; ++x)
-                tma_load_4d(sbase + G::kQ + qs * G::kQBytes + x * G::kQSlab, &q_map, q_full(qs), 0, h * a.group,
-                            b * a.nodes + token0 + j * a.tile_tokens, x);
+                tma_load_4d(sbase + G::kQ + qs * G::kQBytes + x * G::kQSlab, &q_map, q_full(qs), 0, cur.h * a.group,
+                            cur.b * a.nodes + token0 + j * a.tile_tokens, x);
             }
           }
           if (!ok) break;
-          ok = warp_wait(v_empty(vs), ((vc / VS) & 1) ^ 1);
+          ok = warp_wait(v_empty(vr.stage), vr.parity ^ 1);
           if (!ok) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(v_full(vs), live * G::kBlockBytes);
-            issued[1] = vc + 1;
+            mbar_arrive_expect_tx(v_full(vr.stage), live * G::kBlockBytes);
+            issued[1] = ++vc;
           }
           __syncwarp();
           if (lane < live)
-            tma_load_5d(sbase + G::kV + vs * G::kTileBytes + lane * G::kBlockBytes, &kv_map, v_full(vs), 0, 0, 0,
-                        h * (BS / 8), 2 * mine + 1);
-          ++vc;
+            tma_load_5d(sbase + G::kV + vr.stage * G::kTileBytes + lane * G::kBlockBytes, &kv_map, v_full(vr.stage), 0,
+                        0, 0, cur.h * (BS / 8), 2 * mine + 1);
+          vr.next();
         }
       }
       first = 0;
       u += span;
       k = 0;
-      if (u < u_end && ++rp == np) {
-        rp = 0;
-        if (++h == hkv) {
-          h = 0;
-          do {  // units are left, so a later request has nodes
-            ++b;
-            tree_lengths<BS>(a, b, false, len, n);
-          } while (n == 0);
-          tiles = tiles_of(len);
-          np = pairs_of(a, n);
-        }
-      }
+      cur = after;
+      ahead = after_entries;
     }
     // the end: a record without steps
     if (lane == 0) {
@@ -476,131 +560,142 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      struct Walk {
-        int seg = 0;    // segment ordinal
-        int g0 = 0;     // global step at its start
-        int g = 0;      // next step
-        int steps = 0;  // of the segment; 0 before the first
-        bool two = false, end = false;
-        int tail = 0;   // len - first position of the segment's first tile
-      };
-      Walk sw, pw;
-      int qc = 0, q_seg = 0;     // query tiles used by earlier segments, by this one
-      int kc = 0, vc = 0;        // K / V tiles used so far
-      int q_commits[2] = {0, 0};
-      bool ok = true;
-      // the segment of step w.g; false on a time-out
-      auto enter = [&](Walk& w) -> bool {
-        while (!w.end && w.g == w.g0 + w.steps) {
-          const int j = w.seg % G::kSegs;
-          if (!mbar_wait(seg_full(j), (w.seg / G::kSegs) & 1)) return false;
-          w.g0 = w.g;
-          w.steps = segs[j].steps;
-          w.two = (segs[j].flags & kTwo) != 0;
-          w.tail = segs[j].len - segs[j].tile0 * kTile;
-          ++w.seg;
-          if (w.steps == 0) w.end = true;
-        }
-        return true;
-      };
-      auto width = [&](const Walk& w, int tile) {  // tokens of the tile, rounded up to 16
-        return min(kTile, ((w.tail - tile * kTile) + 15) & ~15);
-      };
-      auto issue_s = [&]() -> bool {
-        if (!enter(sw)) return false;
-        if (sw.end) return true;
-        const int local = sw.g - sw.g0;
-        if (local == 0) {
-          qc += q_seg;
-          q_seg = sw.two ? 2 : 1;
-        }
-        const int tile = sw.two ? local >> 1 : local;
-        const int rt = sw.two ? local & 1 : 0;
-        const int ks = kc % KS;
-        const int qi = qc + rt;
-        if (!mbar_wait(k_full(ks), (kc / KS) & 1)) return false;
-        if (tile == 0 && !mbar_wait(q_full(qi & 1), (qi >> 1) & 1)) return false;
-        tc::fence_after_sync();
-        const uint32_t kt = sbase + G::kK + ks * G::kTileBytes;
-        const uint32_t qt = sbase + G::kQ + (qi & 1) * G::kQBytes;
-        const uint32_t d = tmem + G::kS + (sw.g & 1) * kTile;
-        const uint32_t id = tc::idesc_bf16(kRows, width(sw, tile), false, false);
+    const uint32_t lead = lane == 0;
+    constexpr uint64_t kHigh = (static_cast<uint64_t>(tc::kSwizzle128B) << 61) | (1ull << 46);
+    constexpr uint64_t kQDesc = kHigh | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 16);
+    constexpr uint64_t kKDesc = kHigh | (static_cast<uint64_t>(G::kGroupStride >> 4) << 32) | (1ull << 16);
+    constexpr uint64_t kVDesc = kHigh | (static_cast<uint64_t>(G::kGroupStride >> 4) << 32) |
+                                (static_cast<uint64_t>(G::kSlabs > 1 ? 1024 >> 4 : 0) << 16);
+    struct Walk {
+      int seg = 0;    // segments entered
+      int g0 = 0;     // global step at the segment's start
+      int g = 0;      // next step
+      int steps = 0;  // of the segment; 0 before the first
+      bool two = false, end = false;
+      int tail = 0;   // positions from the segment's first tile to the request's end
+      int nodes = 0;
+    };
+    Walk sw, pw;
+    Ring<KS> kr;
+    Ring<VS> vr;
+    int qc = 0, q_seg = 0;  // query tiles used by earlier segments, by this one
+    int kc = 0, vc = 0, q_commits0 = 0, q_commits1 = 0;
+    // the segment of step w.g; false on a time-out
+    auto enter = [&](Walk& w) -> bool {
+      while (!w.end && w.g == w.g0 + w.steps) {
+        const int j = w.seg % G::kSegs;
+        if (!warp_wait(seg_full(j), (w.seg / G::kSegs) & 1)) return false;
+        w.g0 = w.g;
+        w.steps = __shfl_sync(kFull, segs[j].steps, 0);
+        w.two = (__shfl_sync(kFull, segs[j].flags, 0) & kTwo) != 0;
+        w.tail = __shfl_sync(kFull, segs[j].len - segs[j].tile0 * kTile, 0);
+        w.nodes = __shfl_sync(kFull, segs[j].n, 0);
+        ++w.seg;
+        if (w.steps == 0) w.end = true;
+      }
+      return true;
+    };
+    auto issue_s = [&]() -> bool {
+      if (!enter(sw)) return false;
+      if (sw.end) return true;
+      const int local = sw.g - sw.g0;
+      if (local == 0) {
+        qc += q_seg;
+        q_seg = sw.two ? 2 : 1;
+      }
+      const int tile = sw.two ? local >> 1 : local;
+      const int rt = sw.two ? local & 1 : 0;
+      const int qi = qc + rt;
+      if (!warp_wait(k_full(kr.stage), kr.parity)) return false;
+      if (tile == 0 && !warp_wait(q_full(qi & 1), (qi >> 1) & 1)) return false;
+      tc::fence_after_sync();
+      const uint64_t kd = kKDesc | ((sbase + G::kK + kr.stage * G::kTileBytes) >> 4);
+      const uint64_t qd = kQDesc | ((sbase + G::kQ + (qi & 1) * G::kQBytes) >> 4);
+      const uint32_t d = tmem + G::kS + (sw.g & 1) * kTile;
+      const int left = sw.tail - tile * kTile;
+      // the tile's tokens, rounded up to 16
+      const uint32_t id = left >= kTile ? tc::idesc_bf16(kRows, kTile, false, false)
+                                        : tc::idesc_bf16(kRows, (left + 15) & ~15, false, false);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int x = i >> 2, kk = i & 3;
-          const uint64_t ad = tc::smem_desc(qt + x * G::kQSlab + kk * 32, 16, 1024, tc::kSwizzle128B);
-          const uint64_t bd = tc::smem_desc(kt + x * 1024 + kk * 32, 16, G::kGroupStride, tc::kSwizzle128B);
-          tc::mma_bf16(d, ad, bd, id, i > 0 ? 1u : 0u);
-        }
-        tc::commit(s_full(sw.g & 1));
-        if (!sw.two || rt == 1) {
-          tc::commit(k_empty(ks));
-          ++kc;
-        }
-        const int last = sw.two ? sw.steps - 2 + rt : sw.steps - 1;
-        if (local == last) {
-          tc::commit(q_empty(qi & 1));
-          ++q_commits[qi & 1];
-        }
-        ++sw.g;
-        return true;
-      };
-      auto issue_pv = [&]() -> bool {
-        const int local = pw.g - pw.g0;
-        const int s = pw.g & 1;
-        const int tile = pw.two ? local >> 1 : local;
-        const int vs = vc % VS;
-        if (!mbar_wait(p_full(s), (pw.g >> 1) & 1)) return false;
-        // the accumulators were read by the segment before; waited for after
-        // P, which bounds how far behind the other warpgroup can be
-        if (local < 2 && pw.seg > 1 && !mbar_wait(o_free, (pw.seg - 2) & 1)) return false;
-        if (!mbar_wait(v_full(vs), (vc / VS) & 1) || !mbar_wait(v_clean(vs), (vc / VS) & 1)) return false;
-        tc::fence_after_sync();
-        const uint32_t vt = sbase + G::kV + vs * G::kTileBytes;
-        const uint32_t p = tmem + G::kS + s * kTile;
-        const uint32_t d = tmem + G::kO + s * D;
-        constexpr uint32_t id = tc::idesc_bf16(kRows, D, false, true);
-        const int steps = width(pw, tile) / 16;
-        for (int i = 0; i < steps; ++i) {
-          const uint64_t bd = tc::smem_desc(vt + 2 * i * G::kGroupStride, G::kSlabs > 1 ? 1024 : 0, G::kGroupStride,
-                                            tc::kSwizzle128B);
-          tc::mma_bf16_ts(d, p + 8 * i, bd, id, local >= 2 || i > 0 ? 1u : 0u);
-        }
-        tc::commit(pv_done(s));
-        if (!pw.two || (local & 1)) {
-          tc::commit(v_empty(vs));
-          ++vc;
-        }
-        ++pw.g;
-        return true;
-      };
-      ok = issue_s() && issue_s();
-      while (ok) {
-        ok = enter(pw);
-        if (!ok || pw.end) break;
-        ok = issue_pv() && issue_s();
+      for (int i = 0; i < D / 16; ++i) {
+        const int x = i >> 2, kk = i & 3;
+        tc::mma_ss(lead, d, qd + ((x * G::kQSlab + kk * 32) >> 4), kd + ((x * 1024 + kk * 32) >> 4), id, i > 0 ? 1u : 0u);
       }
-      if (!ok) give_up();
-      // every issued product has finished before tensor memory is released,
-      // and every commit's arrival has landed before shared memory goes away
-      tc::commit(drain);
-      mbar_wait_bounded(drain, 0, kWaitLimitNs);
-      auto wait_last = [&](uint32_t at, int commits) {
-        if (commits > 0) mbar_wait_bounded(at, (commits - 1) & 1, kWaitLimitNs);
-      };
-      for (int st = 0; st < KS; ++st) wait_last(k_empty(st), kc > st ? (kc - st + KS - 1) / KS : 0);
-      for (int st = 0; st < VS; ++st) wait_last(v_empty(st), vc > st ? (vc - st + VS - 1) / VS : 0);
-      for (int j = 0; j < 2; ++j) {
-        wait_last(q_empty(j), q_commits[j]);
-        wait_last(pv_done(j), (pw.g + 1 - j) >> 1);
-        wait_last(s_full(j), (sw.g + 1 - j) >> 1);
+      tc::commit_by(lead, s_full(sw.g & 1));
+      if (!sw.two || rt == 1) {
+        tc::commit_by(lead, k_empty(kr.stage));
+        kr.next();
+        ++kc;
       }
+      if (local >= sw.steps - (sw.two ? 2 : 1)) {  // the row tile's last S
+        tc::commit_by(lead, q_empty(qi & 1));
+        if (qi & 1) ++q_commits1;
+        else ++q_commits0;
+      }
+      ++sw.g;
+      return true;
+    };
+    auto issue_pv = [&]() -> bool {
+      const int local = pw.g - pw.g0;
+      const int s = pw.g & 1;
+      const int tile = pw.two ? local >> 1 : local;
+      const int left = pw.tail - tile * kTile;
+      if (!warp_wait(v_full(vr.stage), vr.parity)) return false;
+      if (left < pw.nodes + kTile && !warp_wait(v_clean(vr.stage), vr.parity)) return false;  // see the cleaning warps
+      if (!warp_wait(p_full(s), (pw.g >> 1) & 1)) return false;
+      // the accumulator has been read at the end of the segment before;
+      // waited for after P, which bounds how far behind its readers can be
+      if (local < 2 && pw.seg > 1 && !warp_wait(o_free(s), (pw.seg - 2) & 1)) return false;
+      tc::fence_after_sync();
+      const uint64_t vd = kVDesc | ((sbase + G::kV + vr.stage * G::kTileBytes) >> 4);
+      const uint32_t p = tmem + G::kS + s * kTile;
+      const uint32_t d = tmem + G::kO + s * D;
+      constexpr uint32_t id = tc::idesc_bf16(kRows, D, false, true);
+      const uint32_t more = local >= 2;
+      if (left > kTile - 16) {
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          tc::mma_ts(lead, d, p + 8 * i, vd + ((2 * i * G::kGroupStride) >> 4), id, i > 0 ? 1u : more);
+      } else {
+        for (int i = 0; i < (left + 15) / 16; ++i)
+          tc::mma_ts(lead, d, p + 8 * i, vd + ((2 * i * G::kGroupStride) >> 4), id, i > 0 ? 1u : more);
+      }
+      tc::commit_by(lead, pv_done(s));
+      if (!pw.two || (local & 1)) {
+        tc::commit_by(lead, v_empty(vr.stage));
+        vr.next();
+        ++vc;
+      }
+      ++pw.g;
+      return true;
+    };
+    bool ok = issue_s() && issue_s();
+    while (ok) {
+      ok = enter(pw);
+      if (!ok || pw.end) break;
+      ok = issue_pv() && issue_s();
+    }
+    if (!ok && lane == 0) give_up();
+    __syncwarp();
+    // every issued product has finished before tensor memory is released,
+    // and every commit's arrival has landed before shared memory goes away
+    tc::commit_by(lead, drain);
+    wait(drain, 0);
+    auto wait_last = [&](uint32_t at, int commits) {
+      if (commits > 0) wait(at, (commits - 1) & 1);
+    };
+    for (int st = 0; st < KS; ++st) wait_last(k_empty(st), kc > st ? (kc - st + KS - 1) / KS : 0);
+    for (int st = 0; st < VS; ++st) wait_last(v_empty(st), vc > st ? (vc - st + VS - 1) / VS : 0);
+    wait_last(q_empty(0), q_commits0);
+    wait_last(q_empty(1), q_commits1);
+    for (int j = 0; j < 2; ++j) {
+      wait_last(pv_done(j), (pw.g + 1 - j) >> 1);
+      wait_last(s_full(j), (sw.g + 1 - j) >> 1);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else {
     // ------------------------------------------------- cleaning value tiles
-    int vc = 0;
+    Ring<VS> vr;
     bool ok = true;
     for (int seg = 0; ok; ++seg) {
       const int j = seg % G::kSegs;
@@ -610,9 +705,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (steps == 0) break;
       const int tiles = (segs[j].flags & kTwo) ? steps >> 1 : steps;
       const int len = segs[j].len, base = len - segs[j].n;
-      for (int i = 0; i < tiles && ok; ++i, ++vc) {
-        const int vs = vc % VS;
-        ok = warp_wait(v_full(vs), (vc / VS) & 1);
+      for (int i = 0; i < tiles && ok; ++i, vr.next()) {
+        const int vs = vr.stage;
+        ok = warp_wait(v_full(vs), vr.parity);
         if (!ok) break;
         const int pos0 = (segs[j].tile0 + i) * kTile;
         const int end = min(kTile, len - pos0);  // rows of the request
@@ -643,13 +738,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (found) segs[j].poison = 1;
           fence_proxy_async_smem();  // the rows are read by the MMA
         }
-        mbar_arrive(v_clean(vs));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(v_clean(vs));
+          mbar_arrive(v_empty(vs));  // before the stage's next round there is no next v_clean
+        }
       }
     }
     if (!ok && lane == 0) give_up();
     __syncwarp();
+  }
   } else {
     // ------------------------------------------------- softmax and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int s = (warp - 4) >> 2;     // stream
     const int qd = warp & 3;           // TMEM lane quadrant
     const int row = 32 * qd + lane;    // of the row tile
@@ -684,82 +785,80 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int pos0 = tile * kTile;
           const bool open = pos0 + kTile <= base;  // nothing to mask
           const uint32_t sp = lanes + G::kS + s * kTile;
-          float top = -INFINITY;
+          if (!open || a.negative) {
+            // masks and signs are settled in tensor memory, so that the code
+            // below, which holds the whole row, is the same for every tile
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t bits = open ? kFull : valid ? attended32(mask_row, pos0 + 32 * c, base, n) : 0u;
+              const uint32_t sign = a.negative ? 0x80000000u : 0u;
+              uint32_t x[32];
+              __syncwarp();
+              tc::tmem_ld_x32(sp + 32 * c, x);
+              tc::wait_ld_x32(x);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t r[32];
-            const uint32_t bits = open ? kFull : valid ? attended32(mask_row, pos0 + 32 * c, base, n) : 0u;
-            __syncwarp();
-            tc::tmem_ld_x32(sp + 32 * c, r);
-            tc::wait_ld_x32(r);
-            if (a.negative) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] ^= 0x80000000u;
+              for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1u ? x[e] ^ sign : 0xff800000u;
+              tc::tmem_st_x32(sp + 32 * c, x);
             }
-            if (open) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(r[e]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) top = fmaxf(top, (bits >> e) & 1u ? __uint_as_float(r[e]) : -INFINITY);
-            }
+            tc::wait_st();
           }
-          top *= a.scale_log2;
+          uint32_t r[4][32];  // the row's logits
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::tmem_ld_x32(sp + 32 * c, r[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::wait_ld_x32(r[c]);
+          float tops[8];  // independent chains
+#pragma unroll
+          for (int x = 0; x < 8; ++x) tops[x] = fmaxf(__uint_as_float(r[0][2 * x]), __uint_as_float(r[0][2 * x + 1]));
+#pragma unroll
+          for (int e = 16; e < 128; e += 2)
+            tops[(e >> 1) & 7] = max3(tops[(e >> 1) & 7], __uint_as_float(r[e >> 5][e & 31]), __uint_as_float(r[e >> 5][(e & 31) + 1]));
+          const float top = max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), fmaxf(tops[6], tops[7])) * a.scale_log2;
           const bool over = valid && top > m + kSlack;  // true while m = -inf and something is attended
           if (__any_sync(kFull, over)) {
             const float mn = over ? top : m;
             const float alpha = m == -INFINITY ? 0.f : ex2(m - mn);
-            l = m == mn ? l : l * alpha;
+            const float keep = m == mn ? 1.f : alpha;
             if (!fresh) {
               // O holds the sum through this stream's step before, which is
               // done: the products complete in order, and S of this step is
-              const float keep = m == mn ? 1.f : alpha;
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                const uint32_t oa = lanes + G::kO + s * D + 16 * c;
+                tc::tmem_ld_x16(oa, o);
+                tc::wait_ld_x16(o);
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                const uint32_t oa = lanes + G::kO + s * D + 32 * c;
-                tc::tmem_ld_x32(oa, o);
-                tc::wait_ld_x32(o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                tc::tmem_st_x32(oa, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                tc::tmem_st_x16(oa, o);
               }
             }
+            l *= keep;
             m = mn;
           }
           const float shift = m == -INFINITY ? 0.f : m;
+          const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), shift2 = make_float2(-shift, -shift);
+          float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t r[32];
-            const uint32_t bits = open ? kFull : valid ? attended32(mask_row, pos0 + 32 * c, base, n) : 0u;
-            __syncwarp();
-            tc::tmem_ld_x32(sp + 32 * c, r);
-            tc::wait_ld_x32(r);
-            if (a.negative) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] ^= 0x80000000u;
-            }
-            if (!open) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = (bits >> e) & 1u ? r[e] : 0xff800000u;
-            }
             // probabilities, rounded to bf16; the sum takes the rounded values
             // that the product multiplies, so the weights stay a convex combination
             uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              p[e] = pack_bf16x2(ex2(fmaf(__uint_as_float(r[2 * e]), a.scale_log2, -shift)),
-                                 ex2(fmaf(__uint_as_float(r[2 * e + 1]), a.scale_log2, -shift)));
-              l += bf16lo_to_f32(p[e]);
-              l += bf16hi_to_f32(p[e]);
+              const float2 x = fma2(make_float2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), scale2, shift2);
+              p[e] = pack_bf16x2(ex2(x.x), ex2(x.y));
+              sums[e & 1] = add2(sums[e & 1], make_float2(bf16lo_to_f32(p[e]), bf16hi_to_f32(p[e])));
             }
-            tc::tmem_st_x16(sp + 16 * c, p);  // over columns of S that have been read
+            tc::tmem_st_x16(sp + 16 * c, p);  // over S, which has been read
           }
+          l += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
           tc::wait_st();
           fresh = false;
         }
         tc::fence_before_sync();
-        mbar_arrive(p_full(s));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(s));
       }
       if (!ok) break;
 
@@ -785,30 +884,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * keep0 + o.y * keep1;
         m = mn;
       }
+      // with one row tile each warpgroup writes half of the columns
+      __syncwarp();
       if (work) {
-        const bool complete = (flags & kComplete) != 0;
         const bool poison = segs[j].poison != 0;
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that attends to nothing gets 0
         const int64_t out_row = (static_cast<int64_t>(b) * a.nodes + token) * a.num_q_heads + h * a.group + row_head;
-        const int64_t part_row = (static_cast<int64_t>(blockIdx.x) * 2 + segs[j].slot) * (2 * kRows) + rt * kRows + row;
-        // with one row tile each warpgroup writes half of the columns
+        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + segs[j].slot;
+        const int part_row = rt * kRows + row;
         const int c_begin = two ? 0 : s * (D / 64), c_end = two ? D / 32 : (s + 1) * (D / 64);
+#pragma unroll 1
         for (int c = c_begin; c < c_end; ++c) {
-          uint32_t o[32];
+          const int col = 32 * c;
+          uint32_t own[32], other[32] = {};
           __syncwarp();
-          tc::tmem_ld_x32(lanes + G::kO + s * D + 32 * c, o);
-          tc::wait_ld_x32(o);
+          tc::tmem_ld_x32(lanes + G::kO + s * D + col, own);
+          tc::wait_ld_x32(own);
           if (!two) {
-            uint32_t x[32];
-            tc::tmem_ld_x32(lanes + G::kO + (s ^ 1) * D + 32 * c, x);
-            tc::wait_ld_x32(x);
-            // an accumulator whose stream saw nothing of the row is not read
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint((keep0 > 0.f ? __uint_as_float(o[e]) * keep0 : 0.f) +
-                                     (keep1 > 0.f ? __uint_as_float(x[e]) * keep1 : 0.f));
+            tc::tmem_ld_x32(lanes + G::kO + (s ^ 1) * D + col, other);
+            tc::wait_ld_x32(other);
           }
-          if (valid && poison) {
+          if (!valid) continue;
+          // an accumulator whose stream saw nothing of the row is not used
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = (keep0 > 0.f ? __uint_as_float(own[e]) * keep0 : 0.f) +
+                   (keep1 > 0.f ? __uint_as_float(other[e]) * keep1 : 0.f);
+          if (poison) {
             // values of attended nodes that are not finite
             const int tiles = two ? steps >> 1 : steps;
             const int lo = max(base, tile0 * kTile), hi = min(len, (tile0 + tiles) * kTile);
@@ -818,39 +921,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int block = a.block_tables[static_cast<int64_t>(b) * a.max_blocks + p / BS];
               if (static_cast<unsigned>(block) >= static_cast<unsigned>(a.num_blocks)) continue;
               const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                  a.pool + ((static_cast<int64_t>(block) * 2 + 1) * hkv + h) * BS * D + (p % BS) * D + 32 * c);
+                  a.pool + ((static_cast<int64_t>(block) * 2 + 1) * hkv + h) * BS * D + (p % BS) * D + col);
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const uint32_t w = v[e];
-                if ((w & 0x7f80u) == 0x7f80u) o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + bf16lo_to_f32(w));
-                if ((w & 0x7f800000u) == 0x7f800000u)
-                  o[2 * e + 1] = __float_as_uint(__uint_as_float(o[2 * e + 1]) + bf16hi_to_f32(w));
+                if ((w & 0x7f80u) == 0x7f80u) o[2 * e] += bf16lo_to_f32(w);
+                if ((w & 0x7f800000u) == 0x7f800000u) o[2 * e + 1] += bf16hi_to_f32(w);
               }
             }
           }
-          if (valid && complete) {
-            uint4* to = reinterpret_cast<uint4*>(a.out + out_row * D + 32 * c);
-            // a row that attends to nothing holds no product
+          if (flags & kComplete) {
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
-              to[e] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else if (valid) {
-            float4* to = reinterpret_cast<float4*>(a.part_o + part_row * D + 32 * c);
+            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+            store_64_bytes(a.out + out_row * D + col, w, a.wide_out);
+          } else {
+            float4* to = a.part_o + (slot * (D / 4) + col / 4) * (2 * kRows) + part_row;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              to[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                  __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-            if (c == 0) a.part_ml[part_row] = make_float2(m, l);
+              to[e * (2 * kRows)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
+        if (valid && !(flags & kComplete) && c_begin == 0) a.part_ml[slot * (2 * kRows) + part_row] = make_float2(m, l);
       }
+      __syncwarp();
       tc::fence_before_sync();  // the next segment's first products overwrite O
-      mbar_arrive(o_free);
+      if (two) {
+        mbar_arrive_n(o_free(s), 2);
+      } else {
+        mbar_arrive(o_free(0));
+        mbar_arrive(o_free(1));
+      }
       g0 = g1;
     }
     if (!ok && lane == 0) give_up();
@@ -860,9 +961,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0) {
     // unwind: let every issued load land before the CTA's memory goes away
-    for (int i = max(0, issued[0] - KS); i < issued[0]; ++i) mbar_wait_bounded(k_full(i % KS), (i / KS) & 1, kWaitLimitNs);
-    for (int i = max(0, issued[1] - VS); i < issued[1]; ++i) mbar_wait_bounded(v_full(i % VS), (i / VS) & 1, kWaitLimitNs);
-    for (int i = max(0, issued[2] - 2); i < issued[2]; ++i) mbar_wait_bounded(q_full(i & 1), (i >> 1) & 1, kWaitLimitNs);
+    for (int i = max(0, issued[0] - KS); i < issued[0]; ++i) wait(k_full(i % KS), (i / KS) & 1);
+    for (int i = max(0, issued[1] - VS); i < issued[1]; ++i) wait(v_full(i % VS), (i / VS) & 1);
+    for (int i = max(0, issued[2] - 2); i < issued[2]; ++i) wait(q_full(i & 1), (i >> 1) & 1);
   }
   __syncthreads();
   if (warp == 1) {
@@ -872,72 +973,109 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partials of items cut between CTAs, in the order of the CTAs, and
-// writes the zeros of rows without a node.  One warp per (token, head) row.
+// writes the zeros of rows without a node.  A block takes 32 rows of an item:
+// lane = row, a warp D / 32 column groups of four, so a partial is read 512
+// bytes at a time; the rows are written out through shared memory.
 constexpr int kMergeWarps = 8;
+constexpr int kMergeBatch = 4;  // partials in flight
 
 template <int D, int BS>
-__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeArgs a, int ctas_launched) {
-  constexpr int kPer = D / 32;
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeArgs a, int ctas_launched, int chunks) {
+  constexpr int kGroups = D / 4 / kMergeWarps;  // column groups per warp
+  constexpr int kPitch = D / 2 + 4;             // 32-bit words of a staged row
+  __shared__ int shared[4];  // nodes; first partial's (CTA, slot), number of partials (0: the item is whole)
+  __shared__ uint32_t staged[32 * kPitch];
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int rp = static_cast<int>(blockIdx.x % a.pairs);
-  const int h = static_cast<int>(blockIdx.x / a.pairs % a.num_kv_heads);
-  const int b = static_cast<int>(blockIdx.x / a.pairs / a.num_kv_heads);
-  int len, n;
-  tree_lengths<BS>(a, b, false, len, n);
-  const int token0 = rp * 2 * a.tile_tokens;
-  const int tokens = min(2 * a.tile_tokens, a.nodes - token0);
-  const int tiles = tiles_of(len);
-  const long long total = static_cast<long long>(a.num_kv_heads) * a.prefix_out[a.batch];
-  int c0 = 0, c1 = 0;
-  long long u0 = 0;
-  int ctas = 1;
-  if (token0 < n) {
-    ctas = ctas_for(a, total, ctas_launched);
-    u0 = static_cast<long long>(a.num_kv_heads) * a.prefix_out[b] +
-         (static_cast<long long>(h) * pairs_of(a, n) + rp) * (tiles + a.extra);
-    c0 = cta_of(total, u0, ctas);
-    c1 = cta_of(total, u0 + tiles - 1, ctas);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned at_item = blockIdx.x / chunks;
+  const int chunk = static_cast<int>(blockIdx.x - at_item * chunks);  // 32 rows, within one row tile
+  const unsigned head_item = at_item / a.pairs;
+  const int rp = static_cast<int>(at_item - head_item * a.pairs);
+  const int b = static_cast<int>(head_item / a.num_kv_heads);
+  const int h = static_cast<int>(head_item - b * a.num_kv_heads);
+  const int rt = chunk / (kRows / 32);
+  const int token0 = rp * 2 * a.tile_tokens + rt * a.tile_tokens;
+  if (threadIdx.x == 0) {
+    const int total = a.prefix_out[a.batch], mine = a.prefix_out[b];
+    int len, n;
+    tree_lengths<BS>(a, b, false, len, n);
+    shared[0] = n;
+    shared[3] = 0;
+    if (token0 < n) {
+      const int tiles = tiles_of(len);
+      const int ctas = ctas_for(a, total, ctas_launched);
+      const int u0 = mine + (h * pairs_of(a, n) + rp) * (tiles + a.extra);
+      const int c0 = cta_of(total, u0, ctas), c1 = cta_of(total, u0 + tiles - 1, ctas);
+      shared[1] = c0;
+      shared[2] = range_begin(total, c0, ctas) >= u0 ? 0 : 1;  // later CTAs begin with this item
+      shared[3] = c0 == c1 ? 0 : c1 - c0 + 1;
+    }
   }
-  for (int e = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); e < tokens * a.group; e += gridDim.y * kMergeWarps) {
-    const int tl = e / a.group, head = e - tl * a.group;
-    const int token = token0 + tl;
-    const bool zero = token >= n;
-    if (!zero && c0 == c1) continue;
-    const int rt = tl / a.tile_tokens;
-    const int row = rt * kRows + (tl - rt * a.tile_tokens) * a.group + head;
-    float o[kPer];
+  __syncthreads();
+  const int n = shared[0], parts = shared[3];
+  const int row0 = (chunk % (kRows / 32)) * 32;  // of the row tile
+  const int tile_end = min(a.tile_tokens, a.nodes - token0) * a.group;  // rows of the tile that exist
+  if (row0 >= tile_end || (parts == 0 && token0 + min(a.tile_tokens, a.nodes - token0) <= n)) return;
+  const int row = row0 + lane;
+  const int token = token0 + row / a.group;
+  const bool join = row < tile_end && token < n && parts > 0;
+  float4 o[kGroups];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-    float inv = 0.f;
-    if (!zero) {
-      auto at = [&](int c) -> int64_t {
-        const int slot = c > c0 || range_begin(total, c0, ctas) >= u0 ? 0 : 1;
-        return (static_cast<int64_t>(c) * 2 + slot) * (2 * kRows) + row;
-      };
-      float top = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, a.part_ml[at(c)].x);
+  for (int i = 0; i < kGroups; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (join) {
+    const int c0 = shared[1];
+    auto slot = [&](int f) -> int64_t { return f == 0 ? static_cast<int64_t>(c0) * 2 + shared[2] : static_cast<int64_t>(c0 + f) * 2; };
+    const int part_row = rt * kRows + row;
+    float top = -INFINITY, l = 0.f;
+    for (int f0 = 0; f0 < parts; f0 += kMergeBatch) {
+      float2 ml[kMergeBatch];
+      float4 v[kMergeBatch][kGroups];
+      float mn = top;
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-      float l = 0.f;
-      for (int c = c0; c <= c1; ++c) {
-        const float2 ml = a.part_ml[at(c)];
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // saw nothing of the row
-        const float w = ex2(ml.x - top);
-        l += ml.y * w;
-        const float* from = a.part_o + at(c) * D + lane * kPer;
+      for (int y = 0; y < kMergeBatch; ++y) {
+        const int64_t at = slot(min(f0 + y, parts - 1));
+        ml[y] = a.part_ml[at * (2 * kRows) + part_row];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] += from[i] * w;
+        for (int i = 0; i < kGroups; ++i)
+          v[y][i] = a.part_o[(at * (D / 4) + warp * kGroups + i) * (2 * kRows) + part_row];
       }
-      inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+      for (int y = 0; y < kMergeBatch; ++y)
+        if (f0 + y < parts) mn = fmaxf(mn, ml[y].x);
+      const float keep = top == -INFINITY ? 0.f : ex2(top - mn);
+      l *= keep;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) o[i] = make_float4(o[i].x * keep, o[i].y * keep, o[i].z * keep, o[i].w * keep);
+      top = mn;
+#pragma unroll
+      for (int y = 0; y < kMergeBatch; ++y) {
+        // a partial that saw nothing of the row weighs nothing
+        if (f0 + y >= parts || (ml[y].x == -INFINITY && ml[y].y == 0.f)) continue;
+        const float w = ex2(ml[y].x - mn);
+        l += ml[y].y * w;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+          o[i] = make_float4(fmaf(v[y][i].x, w, o[i].x), fmaf(v[y][i].y, w, o[i].y), fmaf(v[y][i].z, w, o[i].z),
+                             fmaf(v[y][i].w, w, o[i].w));
+      }
     }
-    __nv_bfloat16* to = a.out + ((static_cast<int64_t>(b) * a.nodes + token) * a.num_q_heads + h * a.group + head) * D + lane * kPer;
-    if constexpr (kPer == 4) {
-      *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    } else {
-      *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(o[0] * inv, o[1] * inv);
-    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) o[i] = make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+  }
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i)
+    *reinterpret_cast<uint2*>(staged + lane * kPitch + 2 * (warp * kGroups + i)) =
+        make_uint2(pack_bf16x2(o[i].x, o[i].y), pack_bf16x2(o[i].z, o[i].w));
+  __syncthreads();
+  constexpr int kLanes = D / 8;  // 16-byte pieces of a row
+  for (int x = threadIdx.x; x < 32 * kLanes; x += 32 * kMergeWarps) {
+    const int r = x / kLanes, piece = x % kLanes;
+    const int tl = (row0 + r) / a.group;
+    if (row0 + r >= tile_end || (parts == 0 && token0 + tl < n)) continue;  // no row; or written whole
+    const int64_t out_row = (static_cast<int64_t>(b) * a.nodes + token0 + tl) * a.num_q_heads + h * a.group + (row0 + r - tl * a.group);
+    *reinterpret_cast<uint4*>(a.out + out_row * D + 8 * piece) = *reinterpret_cast<const uint4*>(staged + r * kPitch + 4 * piece);
   }
 }
 
@@ -999,10 +1137,11 @@ int launch_tree(const TreeArgs& a, const void* q, cudaStream_t st) {
   if (rc != PA_OK) return rc;
   const int ctas = std::max(sm_count(), 1);
   PA_CUDA_TRY(launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), G::kTotal, st, kv_map, q_map, a));
-  const int64_t items = static_cast<int64_t>(a.batch) * a.num_kv_heads * a.pairs;
-  const int rows = std::min(2 * a.tile_tokens, a.nodes) * a.group;
-  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>((rows + 4 * kMergeWarps - 1) / (4 * kMergeWarps)));
-  PA_CUDA_TRY(launch_pdl(tree_merge_kernel<D, BS>, grid, dim3(32 * kMergeWarps), 0, st, a, ctas));
+  const int row_tiles = a.nodes > a.tile_tokens ? 2 : 1;
+  const int chunks = row_tiles == 2 ? 2 * kRows / 32 : (a.tile_tokens * a.group + 31) / 32;
+  const int64_t blocks = static_cast<int64_t>(a.batch) * a.num_kv_heads * a.pairs * chunks;
+  PA_CUDA_TRY(launch_pdl(tree_merge_kernel<D, BS>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kMergeWarps), 0, st, a,
+                         ctas, chunks));
   return PA_OK;
 }
 
@@ -1076,11 +1215,12 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   a.extra = 1;
   a.min_units = 1;
   const int64_t longest = std::min(static_cast<int64_t>(max_seq_len), static_cast<int64_t>(max_blocks_per_seq) * block_size);
-  if (static_cast<int64_t>(batch) * a.pairs * ((longest + kTile - 1) / kTile + a.extra) > 0x7fffffffll)
-    return fail(PA_ERR_UNSUPPORTED, "%s: batch * row tiles * tiles of max_seq_len beyond 2^31 - 1", who);
+  if (static_cast<int64_t>(batch) * num_kv_heads * a.pairs > 0x7fffffffll / ((longest + kTile - 1) / kTile + a.extra))
+    return fail(PA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 tiles of work at these sizes", who);
   const Workspace w = workspace_layout(batch, head_dim);
   char* ws = static_cast<char*>(workspace);
-  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.wide_out = aligned(out, 32);
+  a.part_o = reinterpret_cast<float4*>(ws + w.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   a.prefix_out = reinterpret_cast<int*>(ws + w.prefix);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
