@@ -22,8 +22,7 @@
 //
 // The work is split like the balanced decode: all (request, KV head, row-tile
 // pair, tile) units in one line, an equal contiguous share per CTA, items cut
-// between CTAs joined by the merge kernel, which also writes the zeros of the
-// rows that have no node.
+// between CTAs joined by the merge kernel.
 //
 // What a node does not attend to may hold anything.  K: a masked logit is
 // replaced by -inf whatever it was.  V: 0 * NaN would reach every row of the
@@ -66,7 +65,7 @@ struct TreeArgs {
   float4* part_o;     // [CTAs][2][D / 4][2 * kRows] unnormalised, at the row's kept maximum:
                       // a warp, one row per lane, writes 512 bytes in a row
   float2* part_ml;    // [CTAs][2][2 * kRows] (kept maximum, sum)
-  int* prefix_out;    // [batch + 1] units before each request
+  int* shares;        // [CTAs][8]: where each CTA's share begins, for the merge kernel
   int32_t* err;
   int batch, nodes, words, num_q_heads, num_kv_heads, group;
   int tile_tokens;    // tokens per row tile
@@ -154,6 +153,11 @@ __device__ __forceinline__ void unit_prefix(int* prefix, int* sums, const TreeAr
   if (t == 0) prefix[a.batch] = carry;
   __syncthreads();
 }
+
+// What the merge kernel reads of a CTA (kShare ints): the item that its share
+// begins in, and where.
+constexpr int kShare = 8;
+enum ShareField { kShareB, kShareH, kSharePair, kShareTile, kShareTiles, kShareNodes, kShareTotal };
 
 // One CTA's share of one item, published by the producer.
 struct Segment {
@@ -254,19 +258,15 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
-// 64 bytes of one row per thread: whole sectors where the alignment allows.
-__device__ __forceinline__ void store_64_bytes(__nv_bfloat16* to, const uint32_t (&w)[16], int wide) {
+// 32 bytes of one row per thread: a whole sector where the alignment allows.
+__device__ __forceinline__ void store_32_bytes(__nv_bfloat16* to, const uint32_t (&w)[8], int wide) {
   if (wide) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 8)
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * i), "r"(w[i]),
-                   "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
-                   "r"(w[i + 7])
-                   : "memory");
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
   } else {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-      *reinterpret_cast<uint4*>(to + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -392,9 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       found[0] = b;
       found[1] = u_begin - lo;
     }
-    if (blockIdx.x == 0) a.prefix_out[b] = lo;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix_out[a.batch] = total;
   fence_proxy_async_smem();  // the rings' generic writes above, TMA writes below
   tc::fence_before_sync();
   __syncthreads();
@@ -460,6 +458,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       cur.h = item / cur.pairs;
       cur.rp = item - cur.h * cur.pairs;
       ahead = fetch(cur, k);
+    }
+    if (lane == 0) {
+      int* share = a.shares + blockIdx.x * kShare;
+      share[kShareB] = cur.b;
+      share[kShareH] = cur.h;
+      share[kSharePair] = cur.rp;
+      share[kShareTile] = idle ? -1 : k;
+      share[kShareTiles] = cur.tiles;
+      share[kShareNodes] = cur.n;
+      share[kShareTotal] = total;
     }
     int u = u_begin;
     int seg = 0, first = 1, kc = 0, vc = 0, qc = 0;
@@ -595,27 +603,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    auto issue_s = [&]() -> bool {
-      if (!enter(sw)) return false;
-      if (sw.end) return true;
+    // S of step sw.g, whose segment has been entered; `k_there`: its keys were
+    // seen to be there
+    auto issue_s = [&](bool k_there) -> bool {
       const int local = sw.g - sw.g0;
-      if (local == 0) {
-        qc += q_seg;
-        q_seg = sw.two ? 2 : 1;
-      }
       const int tile = sw.two ? local >> 1 : local;
       const int rt = sw.two ? local & 1 : 0;
       const int qi = qc + rt;
-      if (!warp_wait(k_full(kr.stage), kr.parity)) return false;
+      if (!k_there && !warp_wait(k_full(kr.stage), kr.parity)) return false;
       if (tile == 0 && !warp_wait(q_full(qi & 1), (qi >> 1) & 1)) return false;
       tc::fence_after_sync();
       const uint64_t kd = kKDesc | ((sbase + G::kK + kr.stage * G::kTileBytes) >> 4);
       const uint64_t qd = kQDesc | ((sbase + G::kQ + (qi & 1) * G::kQBytes) >> 4);
       const uint32_t d = tmem + G::kS + (sw.g & 1) * kTile;
-      const int left = sw.tail - tile * kTile;
       // the tile's tokens, rounded up to 16
-      const uint32_t id = left >= kTile ? tc::idesc_bf16(kRows, kTile, false, false)
-                                        : tc::idesc_bf16(kRows, (left + 15) & ~15, false, false);
+      const uint32_t id = tc::idesc_bf16(kRows, min(kTile, (sw.tail - tile * kTile + 15) & ~15), false, false);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const int x = i >> 2, kk = i & 3;
@@ -635,17 +637,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++sw.g;
       return true;
     };
-    auto issue_pv = [&]() -> bool {
+    // the segment of the next S; its query tiles follow those of the one before
+    auto enter_s = [&]() -> bool {
+      if (sw.g != sw.g0 + sw.steps || sw.end) return true;
+      qc += q_seg;
+      if (!enter(sw)) return false;
+      q_seg = sw.end ? 0 : sw.two ? 2 : 1;
+      return true;
+    };
+    bool ok = true;
+    for (int i = 0; i < 2 && ok; ++i) ok = enter_s() && (sw.end || issue_s(false));
+    while (ok) {
+      ok = enter(pw);
+      if (!ok || pw.end) break;
       const int local = pw.g - pw.g0;
       const int s = pw.g & 1;
       const int tile = pw.two ? local >> 1 : local;
       const int left = pw.tail - tile * kTile;
-      if (!warp_wait(v_full(vr.stage), vr.parity)) return false;
-      if (left < pw.nodes + kTile && !warp_wait(v_clean(vr.stage), vr.parity)) return false;  // see the cleaning warps
-      if (!warp_wait(p_full(s), (pw.g >> 1) & 1)) return false;
+      // a poll takes its time, so the three of a step are in flight together
+      // (tests: a try may sleep, and the keys may never come)
+      const bool v_there = mbar_test_wait(v_full(vr.stage), vr.parity);
+      const bool p_there = mbar_test_wait(p_full(s), (pw.g >> 1) & 1);
+      const bool k_polled = mbar_test_wait(k_full(kr.stage), kr.parity);
+      const bool k_there = __all_sync(kFull, k_polled);
+      if (!__all_sync(kFull, v_there && p_there))
+        ok = warp_wait(v_full(vr.stage), vr.parity) && warp_wait(p_full(s), (pw.g >> 1) & 1);
+      if (ok && left < pw.nodes + kTile) ok = warp_wait(v_clean(vr.stage), vr.parity);  // see the cleaning warps
       // the accumulator has been read at the end of the segment before;
       // waited for after P, which bounds how far behind its readers can be
-      if (local < 2 && pw.seg > 1 && !warp_wait(o_free(s), (pw.seg - 2) & 1)) return false;
+      if (ok && local < 2 && pw.seg > 1) ok = warp_wait(o_free(s), (pw.seg - 2) & 1);
+      if (!ok) break;
       tc::fence_after_sync();
       const uint64_t vd = kVDesc | ((sbase + G::kV + vr.stage * G::kTileBytes) >> 4);
       const uint32_t p = tmem + G::kS + s * kTile;
@@ -657,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kTile / 16; ++i)
           tc::mma_ts(lead, d, p + 8 * i, vd + ((2 * i * G::kGroupStride) >> 4), id, i > 0 ? 1u : more);
       } else {
+#pragma unroll 1
         for (int i = 0; i < (left + 15) / 16; ++i)
           tc::mma_ts(lead, d, p + 8 * i, vd + ((2 * i * G::kGroupStride) >> 4), id, i > 0 ? 1u : more);
       }
@@ -667,13 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++vc;
       }
       ++pw.g;
-      return true;
-    };
-    bool ok = issue_s() && issue_s();
-    while (ok) {
-      ok = enter(pw);
-      if (!ok || pw.end) break;
-      ok = issue_pv() && issue_s();
+      ok = enter_s();
+      if (ok && !sw.end) ok = issue_s(k_there);
     }
     if (!ok && lane == 0) give_up();
     __syncwarp();
@@ -695,6 +712,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------- cleaning value tiles
+    // first the rows that have no node: 0.  A request's are one piece of out
+    {
+      constexpr int kPiece = 8192;  // bytes per turn of a CTA
+      const int64_t row_bytes = static_cast<int64_t>(a.num_q_heads) * D * 2;
+      const int pieces = static_cast<int>((a.nodes * row_bytes + kPiece - 1) / kPiece);
+      for (int64_t i = blockIdx.x; i < static_cast<int64_t>(a.batch) * pieces; i += gridDim.x) {
+        const int b = static_cast<int>(i / pieces);
+        int len, n;
+        tree_lengths<BS>(a, b, false, len, n);
+        const int64_t lo = max(n * row_bytes, (i - static_cast<int64_t>(b) * pieces) * kPiece);
+        const int64_t hi = min(a.nodes * row_bytes, (i - static_cast<int64_t>(b) * pieces + 1) * kPiece);
+        char* out = reinterpret_cast<char*>(a.out) + b * a.nodes * row_bytes;
+        for (int64_t at = lo + (threadIdx.x - 64) * 16; at < hi; at += 64 * 16)
+          *reinterpret_cast<uint4*>(out + at) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
     Ring<VS> vr;
     bool ok = true;
     for (int seg = 0; ok; ++seg) {
@@ -892,23 +925,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t out_row = (static_cast<int64_t>(b) * a.nodes + token) * a.num_q_heads + h * a.group + row_head;
         const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + segs[j].slot;
         const int part_row = rt * kRows + row;
-        const int c_begin = two ? 0 : s * (D / 64), c_end = two ? D / 32 : (s + 1) * (D / 64);
+        // 16 columns at a time: code that runs once per segment is short, or
+        // fetching it would take longer than running it
+        const int c_begin = two ? 0 : s * (D / 2), c_end = two ? D : (s + 1) * (D / 2);
 #pragma unroll 1
-        for (int c = c_begin; c < c_end; ++c) {
-          const int col = 32 * c;
-          uint32_t own[32], other[32] = {};
+        for (int col = c_begin; col < c_end; col += 16) {
+          uint32_t own[16], other[16] = {};
           __syncwarp();
-          tc::tmem_ld_x32(lanes + G::kO + s * D + col, own);
-          tc::wait_ld_x32(own);
+          tc::tmem_ld_x16(lanes + G::kO + s * D + col, own);
+          tc::wait_ld_x16(own);
           if (!two) {
-            tc::tmem_ld_x32(lanes + G::kO + (s ^ 1) * D + col, other);
-            tc::wait_ld_x32(other);
+            tc::tmem_ld_x16(lanes + G::kO + (s ^ 1) * D + col, other);
+            tc::wait_ld_x16(other);
           }
           if (!valid) continue;
           // an accumulator whose stream saw nothing of the row is not used
-          float o[32];
+          float o[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < 16; ++e)
             o[e] = (keep0 > 0.f ? __uint_as_float(own[e]) * keep0 : 0.f) +
                    (keep1 > 0.f ? __uint_as_float(other[e]) * keep1 : 0.f);
           if (poison) {
@@ -920,25 +954,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!((mask_row[i >> 5] >> (i & 31)) & 1u)) continue;
               const int block = a.block_tables[static_cast<int64_t>(b) * a.max_blocks + p / BS];
               if (static_cast<unsigned>(block) >= static_cast<unsigned>(a.num_blocks)) continue;
-              const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                  a.pool + ((static_cast<int64_t>(block) * 2 + 1) * hkv + h) * BS * D + (p % BS) * D + col);
+              const __nv_bfloat16* v = a.pool + ((static_cast<int64_t>(block) * 2 + 1) * hkv + h) * BS * D + (p % BS) * D + col;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const uint32_t w = v[e];
-                if ((w & 0x7f80u) == 0x7f80u) o[2 * e] += bf16lo_to_f32(w);
-                if ((w & 0x7f800000u) == 0x7f800000u) o[2 * e + 1] += bf16hi_to_f32(w);
+                const float x = __bfloat162float(v[e]);
+                o[e] += isfinite(x) ? 0.f : x;
               }
             }
           }
           if (flags & kComplete) {
-            uint32_t w[16];
+            uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-            store_64_bytes(a.out + out_row * D + col, w, a.wide_out);
+            for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+            store_32_bytes(a.out + out_row * D + col, w, a.wide_out);
           } else {
             float4* to = a.part_o + (slot * (D / 4) + col / 4) * (2 * kRows) + part_row;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 4; ++e)
               to[e * (2 * kRows)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
@@ -972,61 +1004,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the partials of items cut between CTAs, in the order of the CTAs, and
-// writes the zeros of rows without a node.  A block takes 32 rows of an item:
-// lane = row, a warp D / 32 column groups of four, so a partial is read 512
-// bytes at a time; the rows are written out through shared memory.
+// Joins the partials of items cut between CTAs, in the order of the CTAs.  An
+// item is found by the first CTA that continues it; a block takes 32 rows of
+// it: lane = row, a warp D / 32 column groups of four, so a partial is read
+// 512 bytes at a time; the rows are written out through shared memory.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeBatch = 4;  // partials in flight
 
-template <int D, int BS>
-__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeArgs a, int ctas_launched, int chunks) {
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeArgs a, int launched) {
   constexpr int kGroups = D / 4 / kMergeWarps;  // column groups per warp
   constexpr int kPitch = D / 2 + 4;             // 32-bit words of a staged row
-  __shared__ int shared[4];  // nodes; first partial's (CTA, slot), number of partials (0: the item is whole)
   __shared__ uint32_t staged[32 * kPitch];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned at_item = blockIdx.x / chunks;
-  const int chunk = static_cast<int>(blockIdx.x - at_item * chunks);  // 32 rows, within one row tile
-  const unsigned head_item = at_item / a.pairs;
-  const int rp = static_cast<int>(at_item - head_item * a.pairs);
-  const int b = static_cast<int>(head_item / a.num_kv_heads);
-  const int h = static_cast<int>(head_item - b * a.num_kv_heads);
-  const int rt = chunk / (kRows / 32);
-  const int token0 = rp * 2 * a.tile_tokens + rt * a.tile_tokens;
-  if (threadIdx.x == 0) {
-    const int total = a.prefix_out[a.batch], mine = a.prefix_out[b];
-    int len, n;
-    tree_lengths<BS>(a, b, false, len, n);
-    shared[0] = n;
-    shared[3] = 0;
-    if (token0 < n) {
-      const int tiles = tiles_of(len);
-      const int ctas = ctas_for(a, total, ctas_launched);
-      const int u0 = mine + (h * pairs_of(a, n) + rp) * (tiles + a.extra);
-      const int c0 = cta_of(total, u0, ctas), c1 = cta_of(total, u0 + tiles - 1, ctas);
-      shared[1] = c0;
-      shared[2] = range_begin(total, c0, ctas) >= u0 ? 0 : 1;  // later CTAs begin with this item
-      shared[3] = c0 == c1 ? 0 : c1 - c0 + 1;
-    }
-  }
-  __syncthreads();
-  const int n = shared[0], parts = shared[3];
-  const int row0 = (chunk % (kRows / 32)) * 32;  // of the row tile
-  const int tile_end = min(a.tile_tokens, a.nodes - token0) * a.group;  // rows of the tile that exist
-  if (row0 >= tile_end || (parts == 0 && token0 + min(a.tile_tokens, a.nodes - token0) <= n)) return;
-  const int row = row0 + lane;
-  const int token = token0 + row / a.group;
-  const bool join = row < tile_end && token < n && parts > 0;
+  const int c = blockIdx.x + 1;  // the CTA that continues the item
+  const int* share = a.shares + c * kShare;
+  const int first_tile = share[kShareTile], tiles = share[kShareTiles], total = share[kShareTotal];
+  if (first_tile <= 0 || first_tile >= tiles) return;  // it begins with an item, or is idle
+  const int ctas = ctas_for(a, total, launched);
+  const int u0 = range_begin(total, c, ctas) - first_tile;
+  const int before = range_begin(total, c - 1, ctas);
+  if (before > u0) return;  // the CTA before continues it already
+  const int c0 = c - 1;
+  const int parts = cta_of(total, u0 + tiles - 1, ctas) - c0 + 1;
+  const int b = share[kShareB], h = share[kShareH], n = share[kShareNodes];
+  const int rt = blockIdx.y / (kRows / 32);
+  const int token0 = (share[kSharePair] * 2 + rt) * a.tile_tokens;
+  const int row0 = (blockIdx.y % (kRows / 32)) * 32;  // of the row tile
+  const int rows = min(a.tile_tokens, n - token0) * a.group;
+  if (row0 >= rows) return;
   float4 o[kGroups];
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (join) {
-    const int c0 = shared[1];
-    auto slot = [&](int f) -> int64_t { return f == 0 ? static_cast<int64_t>(c0) * 2 + shared[2] : static_cast<int64_t>(c0 + f) * 2; };
-    const int part_row = rt * kRows + row;
+  if (row0 + lane < rows) {
+    const int slot0 = 2 * c0 + (before == u0 ? 0 : 1);  // the later CTAs begin with this item
+    const int part_row = rt * kRows + row0 + lane;
     float top = -INFINITY, l = 0.f;
     for (int f0 = 0; f0 < parts; f0 += kMergeBatch) {
       float2 ml[kMergeBatch];
@@ -1034,7 +1048,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
       float mn = top;
 #pragma unroll
       for (int y = 0; y < kMergeBatch; ++y) {
-        const int64_t at = slot(min(f0 + y, parts - 1));
+        const int f = min(f0 + y, parts - 1);
+        const int64_t at = f == 0 ? slot0 : 2 * (c0 + f);
         ml[y] = a.part_ml[at * (2 * kRows) + part_row];
 #pragma unroll
         for (int i = 0; i < kGroups; ++i)
@@ -1072,8 +1087,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
   constexpr int kLanes = D / 8;  // 16-byte pieces of a row
   for (int x = threadIdx.x; x < 32 * kLanes; x += 32 * kMergeWarps) {
     const int r = x / kLanes, piece = x % kLanes;
+    if (row0 + r >= rows) break;
     const int tl = (row0 + r) / a.group;
-    if (row0 + r >= tile_end || (parts == 0 && token0 + tl < n)) continue;  // no row; or written whole
     const int64_t out_row = (static_cast<int64_t>(b) * a.nodes + token0 + tl) * a.num_q_heads + h * a.group + (row0 + r - tl * a.group);
     *reinterpret_cast<uint4*>(a.out + out_row * D + 8 * piece) = *reinterpret_cast<const uint4*>(staged + r * kPitch + 4 * piece);
   }
@@ -1092,18 +1107,19 @@ int check_tree_shape(const char* who, int batch, int nodes, int hq, int hkv, int
 }
 
 struct Workspace {
-  size_t part_o, part_ml, prefix, bytes;
+  size_t part_o, part_ml, shares, bytes;
 };
 
 // Two partial slots of two row tiles per CTA, one CTA per SM.
-Workspace workspace_layout(int batch, int d) {
-  const size_t rows = static_cast<size_t>(std::max(sm_count(), 1)) * 2 * (2 * kRows);
+Workspace workspace_layout(int d) {
+  const size_t ctas = std::max(sm_count(), 1);
+  const size_t rows = ctas * 2 * (2 * kRows);
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
   Workspace w;
   w.part_o = 0;
   w.part_ml = up(rows * d * sizeof(float));
-  w.prefix = w.part_ml + up(rows * sizeof(float2));
-  w.bytes = w.prefix + up((static_cast<size_t>(batch) + 1) * sizeof(int));
+  w.shares = w.part_ml + up(rows * sizeof(float2));
+  w.bytes = w.shares + up(ctas * kShare * sizeof(int));
   return w;
 }
 
@@ -1137,11 +1153,11 @@ int launch_tree(const TreeArgs& a, const void* q, cudaStream_t st) {
   if (rc != PA_OK) return rc;
   const int ctas = std::max(sm_count(), 1);
   PA_CUDA_TRY(launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), G::kTotal, st, kv_map, q_map, a));
-  const int row_tiles = a.nodes > a.tile_tokens ? 2 : 1;
-  const int chunks = row_tiles == 2 ? 2 * kRows / 32 : (a.tile_tokens * a.group + 31) / 32;
-  const int64_t blocks = static_cast<int64_t>(a.batch) * a.num_kv_heads * a.pairs * chunks;
-  PA_CUDA_TRY(launch_pdl(tree_merge_kernel<D, BS>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kMergeWarps), 0, st, a,
-                         ctas, chunks));
+  if (ctas > 1) {
+    const int chunks = a.nodes > a.tile_tokens ? 2 * kRows / 32 : (a.tile_tokens * a.group + 31) / 32;
+    PA_CUDA_TRY(launch_pdl(tree_merge_kernel<D>, dim3(static_cast<unsigned>(ctas - 1), static_cast<unsigned>(chunks)),
+                           dim3(32 * kMergeWarps), 0, st, a, ctas));
+  }
   return PA_OK;
 }
 
@@ -1159,7 +1175,7 @@ int pa_decode_tree_workspace_size(int batch, int num_nodes, int num_q_heads, int
   const int rc = check_tree_shape("pa_decode_tree_workspace_size", batch, num_nodes, num_q_heads, num_kv_heads,
                                   head_dim, block_size, max_seq_len);
   if (rc != PA_OK) return rc;
-  *bytes_out = workspace_layout(batch, head_dim).bytes;
+  *bytes_out = workspace_layout(head_dim).bytes;
   return PA_OK;
 }
 
@@ -1217,12 +1233,12 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   const int64_t longest = std::min(static_cast<int64_t>(max_seq_len), static_cast<int64_t>(max_blocks_per_seq) * block_size);
   if (static_cast<int64_t>(batch) * num_kv_heads * a.pairs > 0x7fffffffll / ((longest + kTile - 1) / kTile + a.extra))
     return fail(PA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 tiles of work at these sizes", who);
-  const Workspace w = workspace_layout(batch, head_dim);
+  const Workspace w = workspace_layout(head_dim);
   char* ws = static_cast<char*>(workspace);
   a.wide_out = aligned(out, 32);
   a.part_o = reinterpret_cast<float4*>(ws + w.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
-  a.prefix_out = reinterpret_cast<int*>(ws + w.prefix);
+  a.shares = reinterpret_cast<int*>(ws + w.shares);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (head_dim == 128) return block_size == 16 ? launch_tree<128, 16>(a, q, st) : launch_tree<128, 32>(a, q, st);
   return block_size == 16 ? launch_tree<64, 16>(a, q, st) : launch_tree<64, 32>(a, q, st);
