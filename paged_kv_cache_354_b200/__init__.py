@@ -346,15 +346,20 @@ def pa_decode_append(out, q, kv_pool, key, value, slot_mapping, block_tables, se
 # --------------------------------------------------------------------------
 # tree speculation
 # --------------------------------------------------------------------------
-def _on_one_device(where, *tensors):
-    """The CUDA device all tensors (None skipped) are on."""
-    device = None
-    for t in tensors:
-        if t is not None and t.is_cuda:
-            if device is None:
-                device = t.device
-            elif t.device != device:
-                raise ValueError(f"{where}: tensors on {device} and {t.device}")
+def _on_device(where, device, dtype, **tensors):
+    """Check the tensors (None skipped) like ``_require`` and that all are on
+    CUDA device ``device`` (-1: not known yet); returns its index.  These
+    calls run between two decoding steps, so the checks are kept cheap."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+            _require(t, dtype, name)
+        index = t.get_device()
+        if index != device:
+            if device >= 0:
+                raise ValueError(f"{where}: {name} is on cuda:{index}, other tensors on cuda:{device}")
+            device = index
     return device
 
 
@@ -362,13 +367,14 @@ def _launch(where, device, stream, fn, *args):
     """Call fn(*args, stream) with ``device`` current."""
     import torch
 
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, stream.cuda_stream), where)
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream.cuda_stream), where)
+            status = fn(*args, raw)
+    if status != PA_OK:
+        _check(status, where)
 
 
 def _adr(t):
@@ -391,18 +397,12 @@ def pa_plan_append(block_tables, blocks_held, free_blocks, num_free, seq_lens, n
     seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
     blocks_held_out = blocks_held if blocks_held_out is None else blocks_held_out
     num_free_out = num_free if num_free_out is None else num_free_out
-    i32 = torch.int32
-    for t, name in ((block_tables, "block_tables"), (blocks_held, "blocks_held"), (free_blocks, "free_blocks"),
-                    (num_free, "num_free"), (seq_lens, "seq_lens"), (new_tokens, "new_tokens"),
-                    (positions, "positions"), (seq_lens_out, "seq_lens_out"), (blocks_held_out, "blocks_held_out"),
-                    (num_free_out, "num_free_out"), (depths, "depths"), (token_starts, "token_starts"),
-                    (appended_out, "appended_out"), (status_out, "status_out")):
-        if t is not None:
-            _require(t, i32, name)
-    _require(slot_mapping, torch.int64, "slot_mapping")
-    device = _on_one_device(where, block_tables, blocks_held, free_blocks, num_free, seq_lens, new_tokens, positions,
-                            slot_mapping, seq_lens_out, blocks_held_out, num_free_out, depths, token_starts, appended_out,
-                            status_out)
+    device = _on_device(where, -1, torch.int32, block_tables=block_tables, blocks_held=blocks_held,
+                        free_blocks=free_blocks, num_free=num_free, seq_lens=seq_lens, new_tokens=new_tokens,
+                        positions=positions, seq_lens_out=seq_lens_out, blocks_held_out=blocks_held_out,
+                        num_free_out=num_free_out, depths=depths, token_starts=token_starts,
+                        appended_out=appended_out, status_out=status_out)
+    _on_device(where, device, torch.int64, slot_mapping=slot_mapping)
     b, width = block_tables.shape
     per_request = (b,)
     padded = slot_mapping.dim() == 2
@@ -428,17 +428,22 @@ def pa_plan_append(block_tables, blocks_held, free_blocks, num_free, seq_lens, n
             _adr(appended_out), _adr(status_out), b, most, slot_mapping.numel(), free_blocks.shape[0], int(block_size), width)
 
 
-def _token_rows(t, dtype, name):
-    """Token stride of a [tokens, heads, head_dim] tensor whose heads lie together."""
-    if t.dtype != dtype:
+def _token_rows(where, device, dtype, name, t):
+    """(device, shape, token stride) of a [tokens, heads, head_dim] tensor
+    whose tokens may be strided but whose heads lie together."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
-    n, h, d = t.shape
+    index = t.get_device()
+    if device >= 0 and index != device:
+        raise ValueError(f"{where}: {name} is on cuda:{index}, other tensors on cuda:{device}")
+    shape = t.shape
+    n, h, d = shape
     s0, s1, s2 = t.stride()
     if n and h and ((d > 1 and s2 != 1) or (h > 1 and s1 != d)):
         raise ValueError(f"{name}: a token's heads must lie together")
-    return s0 if n > 1 else h * d
+    return index, shape, (s0 if n > 1 else h * d)
 
 
 def pa_norm_rope_and_cache(q_out, q, k, v, kv_pool, slot_mapping, positions, cos_sin, q_weight=None, k_weight=None,
@@ -451,43 +456,43 @@ def pa_norm_rope_and_cache(q_out, q, k, v, kv_pool, slot_mapping, positions, cos
 
     where = "pa_norm_rope_and_cache"
     bf16 = torch.bfloat16
-    qs, qos, ks = _token_rows(q, bf16, "q"), _token_rows(q_out, bf16, "q_out"), _token_rows(k, bf16, "k")
-    n, hq, d = q.shape
-    hkv = k.shape[1]
+    device, q_shape, qs = _token_rows(where, -1, bf16, "q", q)
+    _, q_out_shape, qos = _token_rows(where, device, bf16, "q_out", q_out)
+    _, k_shape, ks = _token_rows(where, device, bf16, "k", k)
+    n, hq, d = q_shape
+    hkv = k_shape[1]
     vs = kos = 0
     blocks = block_size = 0
-    if q_out.shape != q.shape or k.shape != (n, hkv, d):
+    if q_out_shape != q_shape or k_shape != (n, hkv, d):
         raise ValueError(f"{where}: shape mismatch")
-    if kv_pool is not None:
-        _require(kv_pool, bf16, "kv_pool")
-        _require(slot_mapping, torch.int64, "slot_mapping")
-        vs = _token_rows(v, bf16, "v")
+    if kv_pool is None:
+        v = slot_mapping = None
+    else:
+        _on_device(where, device, bf16, kv_pool=kv_pool)
+        _on_device(where, device, torch.int64, slot_mapping=slot_mapping)
+        _, v_shape, vs = _token_rows(where, device, bf16, "v", v)
         blocks, two, pool_heads, block_size, pool_dim = kv_pool.shape
-        if v.shape != k.shape or slot_mapping.numel() != n or (two, pool_heads, pool_dim) != (2, hkv, d):
+        if v_shape != k_shape or slot_mapping.numel() != n or (two, pool_heads, pool_dim) != (2, hkv, d):
             raise ValueError(f"{where}: shape mismatch")
     if k_out is not None:
-        kos = _token_rows(k_out, bf16, "k_out")
-        if k_out.shape != k.shape:
+        _, k_out_shape, kos = _token_rows(where, device, bf16, "k_out", k_out)
+        if k_out_shape != k_shape:
             raise ValueError(f"{where}: shape mismatch")
     most = rotary = 0
     if cos_sin is not None:
-        _require(cos_sin, torch.float32, "cos_sin")
+        _on_device(where, device, torch.float32, cos_sin=cos_sin)
         most, rotary = cos_sin.shape
     if positions is not None:
-        _require(positions, torch.int32, "positions")
+        _on_device(where, device, torch.int32, positions=positions)
         if positions.numel() != n:
             raise ValueError(f"{where}: shape mismatch")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _require(w, bf16, name)
-            if w.shape != (d,):
-                raise ValueError(f"{where}: shape mismatch")
-    device = _on_one_device(where, q, q_out, k, k_out, v if kv_pool is not None else None, kv_pool,
-                            slot_mapping if kv_pool is not None else None, positions, cos_sin, q_weight, k_weight)
+    if q_weight is not None or k_weight is not None:
+        _on_device(where, device, bf16, q_weight=q_weight, k_weight=k_weight)
+        if (q_weight is not None and q_weight.shape != (d,)) or (k_weight is not None and k_weight.shape != (d,)):
+            raise ValueError(f"{where}: shape mismatch")
     _launch(where, device, stream, lib.pa_norm_rope_and_cache, _adr(q_out), qos, _adr(k_out), kos, _adr(kv_pool),
-            _adr(q), qs, _adr(k), ks, _adr(v) if kv_pool is not None else None, vs, _adr(q_weight), _adr(k_weight),
-            float(eps), _adr(cos_sin), most, rotary, 1 if interleaved else 0, _adr(positions),
-            _adr(slot_mapping) if kv_pool is not None else None, n, hq, hkv, d, blocks, block_size)
+            _adr(q), qs, _adr(k), ks, _adr(v), vs, _adr(q_weight), _adr(k_weight), eps, _adr(cos_sin), most, rotary,
+            1 if interleaved else 0, _adr(positions), _adr(slot_mapping), n, hq, hkv, d, blocks, block_size)
 
 
 def pa_decode_tree_workspace_size(batch, num_nodes, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len):
@@ -505,15 +510,14 @@ def pa_decode_tree(out, q, kv_pool, tree_mask, block_tables, seq_lens, max_seq_l
     import torch
 
     where = "pa_decode_tree"
-    _require(out, torch.bfloat16, "out", pinned_ok=True)
-    _require(q, torch.bfloat16, "q")
-    _require(kv_pool, torch.bfloat16, "kv_pool")
-    _require(tree_mask, torch.int32, "tree_mask")
-    _require(block_tables, torch.int32, "block_tables")
-    _require(seq_lens, torch.int32, "seq_lens")
-    _require(workspace, torch.uint8, "workspace")
-    if tree_lens is not None:
-        _require(tree_lens, torch.int32, "tree_lens")
+    device = _on_device(where, -1, torch.bfloat16, q=q, kv_pool=kv_pool)
+    if out.is_cuda:
+        _on_device(where, device, torch.bfloat16, out=out)
+    else:
+        _require(out, torch.bfloat16, "out", pinned_ok=True)
+    _on_device(where, device, torch.int32, tree_mask=tree_mask, block_tables=block_tables, seq_lens=seq_lens,
+               tree_lens=tree_lens)
+    _on_device(where, device, torch.uint8, workspace=workspace)
     nb, two, hkv, bs, d = kv_pool.shape
     b, t, hq, dq = q.shape
     rows = (t, (t + 31) // 32)
@@ -521,7 +525,6 @@ def pa_decode_tree(out, q, kv_pool, tree_mask, block_tables, seq_lens, max_seq_l
             or seq_lens.shape != (b,) or (tree_lens is not None and tree_lens.shape != (b,))
             or tree_mask.shape not in (rows, (b,) + rows)):
         raise ValueError(f"{where}: shape mismatch")
-    device = _on_one_device(where, q, out, kv_pool, tree_mask, block_tables, seq_lens, workspace, tree_lens)
     _launch(where, device, stream, lib.pa_decode_tree, _adr(out), _adr(q), _adr(kv_pool), _adr(tree_mask),
             1 if tree_mask.dim() == 3 else 0, _adr(block_tables), _adr(seq_lens), _adr(tree_lens), b, t, hq, hkv, d,
             bs, nb, block_tables.shape[1], int(max_seq_len), float(scale), _adr(workspace), workspace.numel())
@@ -537,11 +540,9 @@ def pa_tree_accept(kv_pool, path, accept_lens, block_tables, seq_lens, tree_lens
     import torch
 
     where = "pa_tree_accept"
-    _require(kv_pool, torch.bfloat16, "kv_pool")
-    for t, name in ((path, "path"), (accept_lens, "accept_lens"), (block_tables, "block_tables"),
-                    (seq_lens, "seq_lens"), (tree_lens, "tree_lens"), (seq_lens_out, "seq_lens_out")):
-        if t is not None:
-            _require(t, torch.int32, name)
+    device = _on_device(where, -1, torch.bfloat16, kv_pool=kv_pool)
+    _on_device(where, device, torch.int32, path=path, accept_lens=accept_lens, block_tables=block_tables,
+               seq_lens=seq_lens, tree_lens=tree_lens, seq_lens_out=seq_lens_out)
     nb, two, hkv, bs, d = kv_pool.shape
     b, most = path.shape
     if (two != 2 or accept_lens.shape != (b,) or seq_lens.shape != (b,) or block_tables.shape[0] != b
@@ -551,7 +552,6 @@ def pa_tree_accept(kv_pool, path, accept_lens, block_tables, seq_lens, tree_lens
     if tree_lens is None and num_nodes is None:
         raise ValueError(f"{where}: tree_lens or num_nodes")
     nodes = 0x7fffffff if num_nodes is None else int(num_nodes)
-    device = _on_one_device(where, kv_pool, path, accept_lens, block_tables, seq_lens, tree_lens, seq_lens_out)
     _launch(where, device, stream, lib.pa_tree_accept, _adr(kv_pool), _adr(path), _adr(accept_lens), _adr(tree_lens),
             _adr(block_tables), _adr(seq_lens), _adr(seq_lens_out), b, nodes, most, nb, hkv, bs, d,
             block_tables.shape[1])

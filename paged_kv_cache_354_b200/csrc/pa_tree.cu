@@ -50,6 +50,10 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kTile = 128;     // positions per unit of work
 constexpr int kRows = 128;     // rows of a row tile: TMEM lanes
 constexpr int kThreads = 384;  // producer, MMA and two cleaning warps; two softmax warpgroups
+// Warps 0 and 1 clean value tiles.  The issuing and the loading warp sit on
+// the quarters of the SM whose softmax warps own rows 64 to 127: with up to
+// 64 rows those are idle, and nothing competes with the issue.
+constexpr int kProducer = 2, kIssuer = 3;
 constexpr int kMaxBatch = 32768;
 constexpr float kSlack = 8.f;  // log2 units a row's kept maximum may lag: probabilities stay <= 256
 
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensor_map(&kv_map);
     prefetch_tensor_map(&q_map);
   }
-  if (warp == 1) {
+  if (warp == kIssuer) {
     __syncwarp();
     tc::tmem_alloc(smem_u32(tmem_slot), G::kTmemCols);
     tc::tmem_relinquish();
@@ -405,11 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
   };
 
-  // a row's 128 logits stay in registers: the softmax warpgroups take the
-  // ones that the other four warps do not need, 88 + 2 * 208 = 3 * 168
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 0) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------ producer
     // walks the CTA's units; real segments are published in a ring of
     // records.  A record is overwritten kSegs segments later: by then at
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == kIssuer) {
     // ----------------------------------------------------------- MMA issue
     const uint32_t lead = lane == 0;
     constexpr uint64_t kHigh = (static_cast<uint64_t>(tc::kSwizzle128B) << 61) | (1ull << 46);
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t lo = max(n * row_bytes, (i - static_cast<int64_t>(b) * pieces) * kPiece);
         const int64_t hi = min(a.nodes * row_bytes, (i - static_cast<int64_t>(b) * pieces + 1) * kPiece);
         char* out = reinterpret_cast<char*>(a.out) + b * a.nodes * row_bytes;
-        for (int64_t at = lo + (threadIdx.x - 64) * 16; at < hi; at += 64 * 16)
+        for (int64_t at = lo + threadIdx.x * 16; at < hi; at += 64 * 16)
           *reinterpret_cast<uint4*>(out + at) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vt = sbase + G::kV + vs * G::kTileBytes;
           constexpr int kChunks = D / 8;  // 16-byte chunks of a row
           bool found = false;
-          for (int e = (threadIdx.x - 64) + from * kChunks; e < pad * kChunks; e += 64) {
+          for (int e = threadIdx.x + from * kChunks; e < pad * kChunks; e += 64) {
             const int row = e / kChunks, c = e % kChunks;
             const uint32_t at = vt + (row >> 3) * G::kGroupStride + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16;
             uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -783,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
     // ------------------------------------------------- softmax and epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    
     const int s = (warp - 4) >> 2;     // stream
     const int qd = warp & 3;           // TMEM lane quadrant
     const int row = 32 * qd + lane;    // of the row tile
@@ -835,18 +836,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::wait_st();
           }
-          uint32_t r[4][32];  // the row's logits
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // independent chains
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t r[2][32];
+            tc::tmem_ld_x32(sp + 64 * c, r[0]);
+            tc::tmem_ld_x32(sp + 64 * c + 32, r[1]);
+            tc::wait_ld_x32(r[0]);
+            tc::wait_ld_x32(r[1]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tc::tmem_ld_x32(sp + 32 * c, r[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc::wait_ld_x32(r[c]);
-          float tops[8];  // independent chains
-#pragma unroll
-          for (int x = 0; x < 8; ++x) tops[x] = fmaxf(__uint_as_float(r[0][2 * x]), __uint_as_float(r[0][2 * x + 1]));
-#pragma unroll
-          for (int e = 16; e < 128; e += 2)
-            tops[(e >> 1) & 7] = max3(tops[(e >> 1) & 7], __uint_as_float(r[e >> 5][e & 31]), __uint_as_float(r[e >> 5][(e & 31) + 1]));
-          const float top = max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), fmaxf(tops[6], tops[7])) * a.scale_log2;
+            for (int e = 0; e < 64; e += 2)
+              tops[(e >> 1) & 3] = max3(tops[(e >> 1) & 3], __uint_as_float(r[e >> 5][e & 31]), __uint_as_float(r[e >> 5][(e & 31) + 1]));
+          }
+          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * a.scale_log2;
           const bool over = valid && top > m + kSlack;  // true while m = -inf and something is attended
           if (__any_sync(kFull, over)) {
             const float mn = over ? top : m;
@@ -872,18 +874,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float shift = m == -INFINITY ? 0.f : m;
           const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), shift2 = make_float2(-shift, -shift);
           float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t r[2][32];
+            tc::tmem_ld_x32(sp + 64 * c, r[0]);
+            tc::tmem_ld_x32(sp + 64 * c + 32, r[1]);
+            tc::wait_ld_x32(r[0]);
+            tc::wait_ld_x32(r[1]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // probabilities, rounded to bf16; the sum takes the rounded values
-            // that the product multiplies, so the weights stay a convex combination
-            uint32_t p[16];
+            for (int u = 0; u < 2; ++u) {
+              uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 x = fma2(make_float2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), scale2, shift2);
-              p[e] = pack_bf16x2(ex2(x.x), ex2(x.y));
-              sums[e & 1] = add2(sums[e & 1], make_float2(bf16lo_to_f32(p[e]), bf16hi_to_f32(p[e])));
+              for (int e = 0; e < 16; ++e) {
+                const float2 x = fma2(make_float2(__uint_as_float(r[u][2 * e]), __uint_as_float(r[u][2 * e + 1])), scale2, shift2);
+                p[e] = pack_bf16x2(ex2(x.x), ex2(x.y));
+                sums[e & 1] = add2(sums[e & 1], make_float2(bf16lo_to_f32(p[e]), bf16hi_to_f32(p[e])));
+              }
+              tc::tmem_st_x16(sp + 32 * c + 16 * u, p);  // over S, which has been read
             }
-            tc::tmem_st_x16(sp + 16 * c, p);  // over S, which has been read
           }
           l += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
           tc::wait_st();
@@ -998,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = max(0, issued[2] - 2); i < issued[2]; ++i) wait(q_full(i & 1), (i >> 1) & 1);
   }
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kIssuer) {
     __syncwarp();
     tc::tmem_dealloc(tmem, G::kTmemCols);
   }
@@ -1228,7 +1236,7 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   a.negative = scale < 0.f;
   a.tile_tokens = std::min(kRows / a.group, num_nodes);
   a.pairs = (num_nodes + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
-  a.extra = 1;
+  a.extra = 3;
   a.min_units = 1;
   const int64_t longest = std::min(static_cast<int64_t>(max_seq_len), static_cast<int64_t>(max_blocks_per_seq) * block_size);
   if (static_cast<int64_t>(batch) * num_kv_heads * a.pairs > 0x7fffffffll / ((longest + kTile - 1) / kTile + a.extra))
