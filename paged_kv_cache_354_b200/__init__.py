@@ -346,21 +346,23 @@ def pa_decode_append(out, q, kv_pool, key, value, slot_mapping, block_tables, se
 # --------------------------------------------------------------------------
 # tree speculation
 # --------------------------------------------------------------------------
-def _on_device(where, device, dtype, **tensors):
-    """Check the tensors (None skipped) like ``_require`` and that all are on
-    CUDA device ``device`` (-1: not known yet); returns its index.  These
-    calls run between two decoding steps, so the checks are kept cheap."""
+def _fit(dtype, device, tensors):
+    """Whether all tensors (None skipped) are contiguous, of ``dtype`` and on
+    CUDA device ``device``.  These calls run between two decoding steps, where
+    the checks cost as much as the launch: ``_refuse`` says what is wrong."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()):
+            return False
+    return device >= 0
+
+
+def _refuse(where, dtype, device, **tensors):
+    """Raise for the first tensor that ``_fit`` does not take."""
     for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        if t is not None:
             _require(t, dtype, name)
-        index = t.get_device()
-        if index != device:
-            if device >= 0:
-                raise ValueError(f"{where}: {name} is on cuda:{index}, other tensors on cuda:{device}")
-            device = index
-    return device
+            if t.get_device() != device:
+                raise ValueError(f"{where}: {name} is on cuda:{t.get_device()}, other tensors on cuda:{device}")
 
 
 def _launch(where, device, stream, fn, *args):
@@ -397,12 +399,17 @@ def pa_plan_append(block_tables, blocks_held, free_blocks, num_free, seq_lens, n
     seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
     blocks_held_out = blocks_held if blocks_held_out is None else blocks_held_out
     num_free_out = num_free if num_free_out is None else num_free_out
-    device = _on_device(where, -1, torch.int32, block_tables=block_tables, blocks_held=blocks_held,
-                        free_blocks=free_blocks, num_free=num_free, seq_lens=seq_lens, new_tokens=new_tokens,
-                        positions=positions, seq_lens_out=seq_lens_out, blocks_held_out=blocks_held_out,
-                        num_free_out=num_free_out, depths=depths, token_starts=token_starts,
-                        appended_out=appended_out, status_out=status_out)
-    _on_device(where, device, torch.int64, slot_mapping=slot_mapping)
+    device = block_tables.get_device()
+    if not _fit(torch.int32, device, (block_tables, blocks_held, free_blocks, num_free, seq_lens, new_tokens, positions,
+                                      seq_lens_out, blocks_held_out, num_free_out, depths, token_starts, appended_out,
+                                      status_out)):
+        _refuse(where, torch.int32, device, block_tables=block_tables, blocks_held=blocks_held,
+                free_blocks=free_blocks, num_free=num_free, seq_lens=seq_lens, new_tokens=new_tokens,
+                positions=positions, seq_lens_out=seq_lens_out, blocks_held_out=blocks_held_out,
+                num_free_out=num_free_out, depths=depths, token_starts=token_starts, appended_out=appended_out,
+                status_out=status_out)
+    if not _fit(torch.int64, device, (slot_mapping,)):
+        _refuse(where, torch.int64, device, slot_mapping=slot_mapping)
     b, width = block_tables.shape
     per_request = (b,)
     padded = slot_mapping.dim() == 2
@@ -428,22 +435,23 @@ def pa_plan_append(block_tables, blocks_held, free_blocks, num_free, seq_lens, n
             _adr(appended_out), _adr(status_out), b, most, slot_mapping.numel(), free_blocks.shape[0], int(block_size), width)
 
 
-def _token_rows(where, device, dtype, name, t):
-    """(device, shape, token stride) of a [tokens, heads, head_dim] tensor
-    whose tokens may be strided but whose heads lie together."""
+def _token_rows(where, device, dtype, name, t, shape):
+    """Token stride of a [tokens, heads, head_dim] tensor of ``shape`` whose
+    tokens may be strided but whose heads lie together."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise TypeError(f"{name}: expected a CUDA tensor")
     index = t.get_device()
-    if device >= 0 and index != device:
+    if index < 0:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if index != device:
         raise ValueError(f"{where}: {name} is on cuda:{index}, other tensors on cuda:{device}")
-    shape = t.shape
+    if t.shape != shape:
+        raise ValueError(f"{where}: shape mismatch")
     n, h, d = shape
     s0, s1, s2 = t.stride()
     if n and h and ((d > 1 and s2 != 1) or (h > 1 and s1 != d)):
         raise ValueError(f"{name}: a token's heads must lie together")
-    return index, shape, (s0 if n > 1 else h * d)
+    return s0 if n > 1 else h * d
 
 
 def pa_norm_rope_and_cache(q_out, q, k, v, kv_pool, slot_mapping, positions, cos_sin, q_weight=None, k_weight=None,
@@ -456,38 +464,40 @@ def pa_norm_rope_and_cache(q_out, q, k, v, kv_pool, slot_mapping, positions, cos
 
     where = "pa_norm_rope_and_cache"
     bf16 = torch.bfloat16
-    device, q_shape, qs = _token_rows(where, -1, bf16, "q", q)
-    _, q_out_shape, qos = _token_rows(where, device, bf16, "q_out", q_out)
-    _, k_shape, ks = _token_rows(where, device, bf16, "k", k)
+    device, q_shape, k_shape = q.get_device(), q.shape, k.shape
     n, hq, d = q_shape
     hkv = k_shape[1]
+    qs = _token_rows(where, device, bf16, "q", q, q_shape)
+    qos = _token_rows(where, device, bf16, "q_out", q_out, q_shape)
+    ks = _token_rows(where, device, bf16, "k", k, (n, hkv, d))
     vs = kos = 0
     blocks = block_size = 0
-    if q_out_shape != q_shape or k_shape != (n, hkv, d):
-        raise ValueError(f"{where}: shape mismatch")
     if kv_pool is None:
         v = slot_mapping = None
     else:
-        _on_device(where, device, bf16, kv_pool=kv_pool)
-        _on_device(where, device, torch.int64, slot_mapping=slot_mapping)
-        _, v_shape, vs = _token_rows(where, device, bf16, "v", v)
+        if not _fit(bf16, device, (kv_pool,)):
+            _refuse(where, bf16, device, kv_pool=kv_pool)
+        if not _fit(torch.int64, device, (slot_mapping,)):
+            _refuse(where, torch.int64, device, slot_mapping=slot_mapping)
+        vs = _token_rows(where, device, bf16, "v", v, k_shape)
         blocks, two, pool_heads, block_size, pool_dim = kv_pool.shape
-        if v_shape != k_shape or slot_mapping.numel() != n or (two, pool_heads, pool_dim) != (2, hkv, d):
+        if slot_mapping.numel() != n or (two, pool_heads, pool_dim) != (2, hkv, d):
             raise ValueError(f"{where}: shape mismatch")
     if k_out is not None:
-        _, k_out_shape, kos = _token_rows(where, device, bf16, "k_out", k_out)
-        if k_out_shape != k_shape:
-            raise ValueError(f"{where}: shape mismatch")
+        kos = _token_rows(where, device, bf16, "k_out", k_out, k_shape)
     most = rotary = 0
     if cos_sin is not None:
-        _on_device(where, device, torch.float32, cos_sin=cos_sin)
+        if not _fit(torch.float32, device, (cos_sin,)):
+            _refuse(where, torch.float32, device, cos_sin=cos_sin)
         most, rotary = cos_sin.shape
     if positions is not None:
-        _on_device(where, device, torch.int32, positions=positions)
+        if not _fit(torch.int32, device, (positions,)):
+            _refuse(where, torch.int32, device, positions=positions)
         if positions.numel() != n:
             raise ValueError(f"{where}: shape mismatch")
     if q_weight is not None or k_weight is not None:
-        _on_device(where, device, bf16, q_weight=q_weight, k_weight=k_weight)
+        if not _fit(bf16, device, (q_weight, k_weight)):
+            _refuse(where, bf16, device, q_weight=q_weight, k_weight=k_weight)
         if (q_weight is not None and q_weight.shape != (d,)) or (k_weight is not None and k_weight.shape != (d,)):
             raise ValueError(f"{where}: shape mismatch")
     _launch(where, device, stream, lib.pa_norm_rope_and_cache, _adr(q_out), qos, _adr(k_out), kos, _adr(kv_pool),
@@ -510,14 +520,17 @@ def pa_decode_tree(out, q, kv_pool, tree_mask, block_tables, seq_lens, max_seq_l
     import torch
 
     where = "pa_decode_tree"
-    device = _on_device(where, -1, torch.bfloat16, q=q, kv_pool=kv_pool)
-    if out.is_cuda:
-        _on_device(where, device, torch.bfloat16, out=out)
-    else:
+    device = q.get_device()
+    if not _fit(torch.bfloat16, device, (q, kv_pool, out)):
+        _refuse(where, torch.bfloat16, device, q=q, kv_pool=kv_pool)
         _require(out, torch.bfloat16, "out", pinned_ok=True)
-    _on_device(where, device, torch.int32, tree_mask=tree_mask, block_tables=block_tables, seq_lens=seq_lens,
-               tree_lens=tree_lens)
-    _on_device(where, device, torch.uint8, workspace=workspace)
+        if out.is_cuda:
+            _refuse(where, torch.bfloat16, device, out=out)
+    if not _fit(torch.int32, device, (tree_mask, block_tables, seq_lens, tree_lens)):
+        _refuse(where, torch.int32, device, tree_mask=tree_mask, block_tables=block_tables, seq_lens=seq_lens,
+                tree_lens=tree_lens)
+    if not _fit(torch.uint8, device, (workspace,)):
+        _refuse(where, torch.uint8, device, workspace=workspace)
     nb, two, hkv, bs, d = kv_pool.shape
     b, t, hq, dq = q.shape
     rows = (t, (t + 31) // 32)
@@ -540,9 +553,12 @@ def pa_tree_accept(kv_pool, path, accept_lens, block_tables, seq_lens, tree_lens
     import torch
 
     where = "pa_tree_accept"
-    device = _on_device(where, -1, torch.bfloat16, kv_pool=kv_pool)
-    _on_device(where, device, torch.int32, path=path, accept_lens=accept_lens, block_tables=block_tables,
-               seq_lens=seq_lens, tree_lens=tree_lens, seq_lens_out=seq_lens_out)
+    device = kv_pool.get_device()
+    if not _fit(torch.bfloat16, device, (kv_pool,)):
+        _refuse(where, torch.bfloat16, device, kv_pool=kv_pool)
+    if not _fit(torch.int32, device, (path, accept_lens, block_tables, seq_lens, tree_lens, seq_lens_out)):
+        _refuse(where, torch.int32, device, path=path, accept_lens=accept_lens, block_tables=block_tables,
+                seq_lens=seq_lens, tree_lens=tree_lens, seq_lens_out=seq_lens_out)
     nb, two, hkv, bs, d = kv_pool.shape
     b, most = path.shape
     if (two != 2 or accept_lens.shape != (b,) or seq_lens.shape != (b,) or block_tables.shape[0] != b

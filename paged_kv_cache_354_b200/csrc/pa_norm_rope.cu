@@ -5,12 +5,16 @@
 //
 // Bytes bound it: every query, key and value row is read once and written
 // once.  head_dim / 16 lanes share a row, 16 elements (two 16-byte chunks)
-// each, placed so that both elements of every rotated pair are in one
-// thread: with half-split pairs lane l holds chunks l and l + rotary_dim / 16,
-// with interleaved pairs chunks 2l and 2l + 1; either way it rotates by the
-// angles 8l .. 8l + 7.  The lanes past the rotated chunks take the rest, two
-// by two.  Sums and products are fp32, rounded to bf16 once.
+// each, placed so that both elements of every rotated pair are in one thread:
+// with half-split pairs lane l holds chunks l and l + rotary_dim / 16, with
+// interleaved pairs chunks 2l and 2l + 1; either way it rotates by the angles
+// 8l .. 8l + 7.  The lanes past the rotated chunks take the rest, two by two.
+// A thread takes kRows rows of a token, all their loads in flight at once and
+// the cosines and sines fetched once.  Sums and products are fp32, rounded to
+// bf16 once.
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -33,14 +37,18 @@ struct RopeArgs {
   int max_position, rotary_dim, interleaved;
   const int32_t* positions;
   const int64_t* slots;
-  int64_t total;  // rows: tokens * (q heads + kv heads (k) + kv heads (v, when cached))
-  int num_q_heads, num_kv_heads, rows_per_token;
+  int num_q_heads, num_kv_heads;
+  int64_t num_tokens;
+  int rows_stride;     // groups of lanes per token: ceil(rows_per_token / kRows)
+  int rows_per_token;  // query heads, KV heads (keys), KV heads again (values) when cached
   int block_size;
   int64_t num_slots;
   int32_t* err;
 };
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
+constexpr int kRows = 6;  // rows of a thread
+constexpr int kRopeBlocks = 4;  // per SM, resident
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -57,111 +65,148 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) norm_rope_kernel(const RopeArgs a) {
   constexpr int kLanes = D / 16;  // per row
   pdl_trigger();
   pdl_wait();
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x) / kLanes;
   const int l = threadIdx.x & (kLanes - 1);
-  const bool live = row < a.total;
-  const int64_t token = live ? row / a.rows_per_token : 0;
-  const int r = live ? static_cast<int>(row - token * a.rows_per_token) : 0;
-  const bool is_q = r < a.num_q_heads;
-  const bool is_v = r >= a.num_q_heads + a.num_kv_heads;
-  const int head = is_q ? r : (r - a.num_q_heads) % max(a.num_kv_heads, 1);
-
   // the two chunks of this lane
   const int turned = a.rotary_dim / 16;  // lanes that rotate
-  const bool turns = l < turned && !is_v;
-  int c0, c1;
-  if (l < turned && !a.interleaved) {
-    c0 = l;
-    c1 = l + turned;
-  } else {
-    c0 = 2 * l;
-    c1 = 2 * l + 1;
-  }
-  const __nv_bfloat16* src = is_q ? a.q + token * a.q_stride : is_v ? a.v + token * a.v_stride : a.k + token * a.k_stride;
-  const uint4* from = reinterpret_cast<const uint4*>(src + head * D);
-  int pos = 0;
-  int64_t slot = -1;
-  uint4 u0 = {}, u1 = {};
-  if (live) {
-    u0 = from[c0];
-    u1 = from[c1];
-    if (a.rotary_dim > 0 || a.positions != nullptr) pos = a.positions[token];
-    if (a.pool != nullptr && !is_q) slot = a.slots[token];
-  }
-  const bool beyond = a.rotary_dim > 0 && pos >= a.max_position;
-  const bool padding = pos < 0 || beyond;
-  if (live && l == 0 && r == 0) {
-    if (beyond) flag_error(a.err, PA_DEVERR_POSITION);
-  }
-  if (slot >= a.num_slots) {
-    if (live && l == 0 && !is_v && head == 0) flag_error(a.err, PA_DEVERR_SLOT);
-    slot = -1;
-  }
-  float x0[8], x1[8];
-  unpack8(u0, x0);
-  unpack8(u1, x1);
-  float sum = 0.f;  // of the row's squares; every lane takes part in the shuffles
+  const bool turns = l < turned;
+  const int c0 = turns && !a.interleaved ? l : 2 * l;
+  const int c1 = turns && !a.interleaved ? l + turned : 2 * l + 1;
+  // groups of lanes: (token, first row), the rows of a group `stride` apart
+  const int stride = a.rows_stride;
+  const int64_t groups = a.num_tokens * stride, step = static_cast<int64_t>(gridDim.x) * (kRopeThreads / kLanes);
+  auto token_of = [&](int64_t group) -> int64_t {
+    return group <= 0xffffffffll ? static_cast<unsigned>(group) / static_cast<unsigned>(stride) : group / stride;
+  };
+  int64_t group = (static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x) / kLanes;
+  int64_t token = 0, slot_next = -1;
+  int pos_next = 0;
+  auto fetch = [&](int64_t g) {  // the token's position and slot, a round ahead of its rows
+    token = token_of(g);
+    if (g < groups) {
+      if (a.positions != nullptr) pos_next = a.positions[token];
+      if (a.pool != nullptr) slot_next = a.slots[token];
+    }
+  };
+  fetch(group);
+  // every lane of a warp makes the same rounds: the shuffles need all of them
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / kLanes); first < groups; first += step, group += step) {
+    const int64_t at = token;
+    const int rows = group < groups ? a.rows_per_token : 0;
+    const int r_first = static_cast<int>(group - at * stride);
+    const int pos = pos_next;
+    int64_t slot = slot_next;
+    const __nv_bfloat16* q = a.q + at * a.q_stride;
+    const __nv_bfloat16* k = a.k + at * a.k_stride;
+    const __nv_bfloat16* v = a.v + at * a.v_stride;
+    // rows: queries, keys, and the values when they are cached
+    auto row_at = [&](int r) -> const uint4* {
+      const __nv_bfloat16* p = r < a.num_q_heads ? q + r * D
+                               : r < a.num_q_heads + a.num_kv_heads ? k + (r - a.num_q_heads) * D
+                                                                    : v + (r - a.num_q_heads - a.num_kv_heads) * D;
+      return reinterpret_cast<const uint4*>(p);
+    };
+    uint4 u0[kRows], u1[kRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum += x0[i] * x0[i] + x1[i] * x1[i];
-#pragma unroll
-  for (int off = kLanes / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (!is_v) {
-    const __nv_bfloat16* weight = is_q ? a.q_weight : a.k_weight;
-    if (weight != nullptr) {
-      const float scale = rsqrtf(sum * (1.f / D) + a.eps);
-      float w0[8], w1[8];
-      unpack8(reinterpret_cast<const uint4*>(weight)[c0], w0);
-      unpack8(reinterpret_cast<const uint4*>(weight)[c1], w1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x0[i] = x0[i] * scale * w0[i];
-        x1[i] = x1[i] * scale * w1[i];
+    for (int i = 0; i < kRows; ++i) {
+      const int r = r_first + i * stride;
+      if (r < rows) {
+        const uint4* from = row_at(r);
+        u0[i] = from[c0];
+        u1[i] = from[c1];
+      } else {
+        u0[i] = u1[i] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
-    if (turns && live && !padding) {
+    const bool beyond = a.rotary_dim > 0 && pos >= a.max_position && rows > 0;
+    const bool padding = pos < 0 || beyond;
+    float c[8], s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = 1.f;
+      s[i] = 0.f;
+    }
+    if (turns && !padding && rows > 0) {
       const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim + 8 * l;
-      float c[8], s[8];
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
         *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + i);
         *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(cs + a.rotary_dim / 2 + i);
       }
-      if (a.interleaved) {
+    }
+    fetch(group + step);
+    if (r_first == 0 && l == 0 && rows > 0) {
+      if (beyond) flag_error(a.err, PA_DEVERR_POSITION);
+      if (slot >= a.num_slots) flag_error(a.err, PA_DEVERR_SLOT);
+    }
+    if (slot >= a.num_slots || padding) slot = -1;
+    // key row of head 0 in the pool, in 16-byte chunks
+    const int64_t block = slot / a.block_size;
+    const int64_t pool_row = (block * 2 * a.num_kv_heads) * a.block_size + (slot - block * a.block_size);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p0 = x0[2 * i], q0 = x0[2 * i + 1], p1 = x1[2 * i], q1 = x1[2 * i + 1];
-          x0[2 * i] = p0 * c[i] - q0 * s[i];
-          x0[2 * i + 1] = q0 * c[i] + p0 * s[i];
-          x1[2 * i] = p1 * c[4 + i] - q1 * s[4 + i];
-          x1[2 * i + 1] = q1 * c[4 + i] + p1 * s[4 + i];
-        }
-      } else {
+    for (int i = 0; i < kRows; ++i) {
+      const int r = r_first + i * stride;
+      const bool is_q = r < a.num_q_heads, is_v = r >= a.num_q_heads + a.num_kv_heads;
+      float x0[8], x1[8];
+      unpack8(u0[i], x0);
+      unpack8(u1[i], x1);
+      float sum = 0.f;  // of the row's squares; every lane takes part in the shuffles
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = x0[i], q = x1[i];
-          x0[i] = p * c[i] - q * s[i];
-          x1[i] = q * c[i] + p * s[i];
+      for (int e = 0; e < 8; ++e) sum += x0[e] * x0[e] + x1[e] * x1[e];
+#pragma unroll
+      for (int off = kLanes / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (r >= rows) continue;
+      if (!is_v) {
+        const __nv_bfloat16* weight = is_q ? a.q_weight : a.k_weight;
+        if (weight != nullptr) {
+          const float scale = rsqrtf(sum * (1.f / D) + a.eps);
+          float w0[8], w1[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(weight) + c0), w0);
+          unpack8(__ldg(reinterpret_cast<const uint4*>(weight) + c1), w1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x0[e] = x0[e] * scale * w0[e];
+            x1[e] = x1[e] * scale * w1[e];
+          }
         }
+        if (turns) {
+          if (a.interleaved) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p0 = x0[2 * e], p1 = x0[2 * e + 1], p2 = x1[2 * e], p3 = x1[2 * e + 1];
+              x0[2 * e] = p0 * c[e] - p1 * s[e];
+              x0[2 * e + 1] = p1 * c[e] + p0 * s[e];
+              x1[2 * e] = p2 * c[4 + e] - p3 * s[4 + e];
+              x1[2 * e + 1] = p3 * c[4 + e] + p2 * s[4 + e];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float p0 = x0[e], p1 = x1[e];
+              x0[e] = p0 * c[e] - p1 * s[e];
+              x1[e] = p1 * c[e] + p0 * s[e];
+            }
+          }
+        }
+        u0[i] = padding ? make_uint4(0u, 0u, 0u, 0u) : pack8(x0);
+        u1[i] = padding ? make_uint4(0u, 0u, 0u, 0u) : pack8(x1);
+      }
+      if (is_q || (!is_v && a.k_out != nullptr)) {
+        uint4* to = reinterpret_cast<uint4*>(is_q ? a.q_out + at * a.q_out_stride + r * D
+                                                  : a.k_out + at * a.k_out_stride + (r - a.num_q_heads) * D);
+        to[c0] = u0[i];
+        to[c1] = u1[i];
+      }
+      if (!is_q && slot >= 0) {
+        // heads of keys, then of values: block_size rows apart
+        uint4* to = a.pool + (pool_row + static_cast<int64_t>(r - a.num_q_heads) * a.block_size) * (D / 8);
+        to[c0] = u0[i];
+        to[c1] = u1[i];
       }
     }
-    u0 = padding ? make_uint4(0, 0, 0, 0) : pack8(x0);
-    u1 = padding ? make_uint4(0, 0, 0, 0) : pack8(x1);
-  }
-  if (!live) return;
-  if (is_q || (!is_v && a.k_out != nullptr)) {
-    uint4* to = reinterpret_cast<uint4*>((is_q ? a.q_out + token * a.q_out_stride : a.k_out + token * a.k_out_stride) + head * D);
-    to[c0] = u0;
-    to[c1] = u1;
-  }
-  if (!is_q && slot >= 0 && !padding) {
-    const int64_t block = slot / a.block_size;
-    const int64_t at = ((block * 2 + (is_v ? 1 : 0)) * a.num_kv_heads + head) * a.block_size + (slot - block * a.block_size);
-    a.pool[at * (D / 8) + c0] = u0;
-    a.pool[at * (D / 8) + c1] = u1;
   }
 }
 
@@ -237,12 +282,15 @@ extern "C" int pa_norm_rope_and_cache(pa_bf16* q_out, int64_t q_out_stride, pa_b
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = num_kv_heads;
   a.rows_per_token = num_q_heads + num_kv_heads * (kv_pool ? 2 : 1);
-  a.total = static_cast<int64_t>(num_tokens) * a.rows_per_token;
   a.block_size = block_size;
   a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
   a.err = err;
-  const int64_t grid = (a.total * (head_dim / 16) + kRopeThreads - 1) / kRopeThreads;
-  if (grid > 0x7fffffffll) return fail(PA_ERR_INVALID, "%s: too many tokens", who);
+  a.num_tokens = num_tokens;
+  a.rows_stride = (a.rows_per_token + kRows - 1) / kRows;
+  // as many blocks as are resident, each going round: the position of the next
+  // round's token is there when its rows and angles are asked for
+  const int64_t blocks = (a.num_tokens * a.rows_stride * (head_dim / 16) + kRopeThreads - 1) / kRopeThreads;
+  const int64_t grid = std::min(blocks, static_cast<int64_t>(std::max(sm_count(), 1)) * kRopeBlocks);
   const dim3 g(static_cast<unsigned>(grid));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (head_dim == 128) PA_CUDA_TRY(launch_pdl(norm_rope_kernel<128>, g, dim3(kRopeThreads), 0, st, a));

@@ -4,12 +4,18 @@
 // pa_plan_append is three exclusive sums over the requests -- blocks given
 // back, blocks needed, tokens -- and index arithmetic on them: the k-th block
 // handed out is entry F + R - 1 - k of the free stack (F free before, R given
-// back), so no request waits for another one's pop.  One CTA does all of it.
+// back), so no request waits for another one's pop.  Latency is all the cost:
+// a decoding step is one CTA (64 requests of 16 tokens: 3.8 us); from
+// kPlanSpread slots or kPlanMany requests on a cluster of 8 shares the requests and
+// exchanges its sums through distributed shared memory, and a packed call of
+// that size leaves its slots to a second, wide launch (1000 requests, 256k
+// slots: 328 us on one CTA, 66 us when the cluster wrote the slots).
 //
 // pa_tree_accept moves rows of the pool.  A thread owns one 16-byte column of
 // the rows of one request and walks the path in order: step i writes row i
 // and reads row path[i] >= i, so no row is written before it is read, without
 // any barrier.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "pa_device.cuh"
@@ -42,6 +48,9 @@ struct PlanArgs {
 };
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCluster = 8;
+constexpr int kPlanSpread = 4096;  // slots, or
+constexpr int kPlanMany = 2048;    // requests, from which a cluster is used
 
 struct Sums {
   long long back, need, tokens;
@@ -77,16 +86,45 @@ __device__ __forceinline__ long long warp_inclusive(long long v, int lane) {
   return v;
 }
 
+// Entry of a slot: position p of a request whose tokens begin at `base`.
+__device__ __forceinline__ void write_slot(const PlanArgs& a, int64_t i, int b, int base, int off) {
+  const int p = base + off;
+  const int block = __ldcg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks + p / a.block_size);
+  int64_t slot = -1;
+  if (static_cast<unsigned>(block) < static_cast<unsigned>(a.num_blocks))
+    slot = static_cast<int64_t>(block) * a.block_size + p % a.block_size;
+  else
+    flag_error(a.err, PA_DEVERR_BLOCK_ID);
+  a.slots[i] = slot;
+  a.positions[i] = a.depths != nullptr ? base + a.depths[static_cast<int64_t>(b) * a.depths_stride + off] : p;
+}
+
+// kRanks CTAs (a cluster when more than one); kSlots: this launch writes the slots.
+template <int kRanks, bool kSlots>
 __global__ void __launch_bounds__(kPlanThreads) plan_append_kernel(const PlanArgs a) {
+  namespace cg = cooperative_groups;
   __shared__ long long part[3][32];
-  __shared__ int any_bad;
+  __shared__ long long mine_total[4];  // of this CTA: back, need, tokens, bad
+  // a single CTA keeps what its slots follow from
+  constexpr int kKept = kRanks == 1 ? kPlanMany : 1;
+  __shared__ int kept_len[kKept], kept_count[kKept], kept_start[kKept];
+  auto sync_all = []() {
+    if constexpr (kRanks > 1) cg::this_cluster().sync();
+    else __syncthreads();
+  };
+  int rank = 0;
+  if constexpr (kRanks > 1) rank = static_cast<int>(cg::this_cluster().block_rank());
   pdl_trigger();
-  if (threadIdx.x == 0) any_bad = 0;
   pdl_wait();
-  __syncthreads();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int per = (a.batch + kPlanThreads - 1) / kPlanThreads;
-  const int lo = min(a.batch, t * per), hi = min(a.batch, lo + per);
+  // this thread's requests, a run of them; few requests are spread over all
+  // warps, which take turns at the blocks of theirs
+  const int share = (a.batch + kRanks - 1) / kRanks;  // of the CTA
+  const int per = (share + kPlanThreads - 1) / kPlanThreads;
+  const int spread = per > 1 ? 1 : kPlanThreads / max(share, 1);
+  const int end = min(a.batch, (rank + 1) * share);
+  const int lo = t % spread == 0 ? min(end, rank * share + t / spread * per) : end;
+  const int hi = min(end, lo + per);
   Sums mine{0, 0, 0};
   bool bad = false;
   for (int b = lo; b < hi; ++b) {
@@ -96,94 +134,201 @@ __global__ void __launch_bounds__(kPlanThreads) plan_append_kernel(const PlanArg
     mine.need += s.need;
     mine.tokens += s.tokens;
   }
-  if (bad) any_bad = 1;
-  Sums incl{warp_inclusive(mine.back, lane), warp_inclusive(mine.need, lane), warp_inclusive(mine.tokens, lane)};
+  const int first = a.num_free[0];
+  const Sums incl{warp_inclusive(mine.back, lane), warp_inclusive(mine.need, lane), warp_inclusive(mine.tokens, lane)};
   if (lane == 31) {
     part[0][warp] = incl.back;
     part[1][warp] = incl.need;
     part[2][warp] = incl.tokens;
   }
-  __syncthreads();
+  const int any_bad = __syncthreads_or(bad);
   if (warp < 3) {
     const long long v = warp_inclusive(part[warp][lane], lane);
     part[warp][lane] = v;
+    if (lane == 31) mine_total[warp] = v;
+  } else if (warp == 3 && lane == 0) {
+    mine_total[3] = any_bad;
   }
-  __syncthreads();
-  const long long back = part[0][31], need = part[1][31], tokens = part[2][31];
-  const int first = a.num_free[0];
-  int status = 0;
-  if (any_bad || first < 0 || first + back > a.num_blocks || tokens > a.num_slots) status = PA_DEVERR_PLAN;
-  else if (need > first + back) status = PA_DEVERR_NO_BLOCKS;
+  sync_all();
   Sums at{incl.back - mine.back, incl.need - mine.need, incl.tokens - mine.tokens};
   if (warp > 0) {
     at.back += part[0][warp - 1];
     at.need += part[1][warp - 1];
     at.tokens += part[2][warp - 1];
   }
-  if (t == 0) {
+  long long back = 0, need = 0, tokens = 0, wrong = 0;
+#pragma unroll
+  for (int r = 0; r < kRanks; ++r) {
+    const long long* other = mine_total;
+    if constexpr (kRanks > 1) other = cg::this_cluster().map_shared_rank(mine_total, r);
+    if (r < rank) {
+      at.back += other[0];
+      at.need += other[1];
+      at.tokens += other[2];
+    }
+    back += other[0];
+    need += other[1];
+    tokens += other[2];
+    wrong += other[3];
+  }
+  int status = 0;
+  if (wrong || first < 0 || first + back > a.num_blocks || tokens > a.num_slots) status = PA_DEVERR_PLAN;
+  else if (need > first + back) status = PA_DEVERR_NO_BLOCKS;
+  // returned blocks go on the stack before any block is taken from it; a
+  // warp copies its requests' blocks one request after the other
+  if (status == 0 && back > 0) {
+    long long to = first + at.back;
+    for (int i = 0; i < per; ++i) {
+      const int b = lo + i;
+      const int count = b < hi && a.new_tokens[b] < 0 ? a.blocks_held[b] : 0;
+      for (unsigned left = __ballot_sync(kFull, count > 0); left != 0; left &= left - 1) {
+        const int from = __ffs(left) - 1;
+        const int cb = __shfl_sync(kFull, b, from), cn = __shfl_sync(kFull, count, from);
+        const long long ct = __shfl_sync(kFull, to, from);
+        for (int x = lane; x < cn; x += 32) a.free_blocks[ct + x] = a.block_tables[static_cast<int64_t>(cb) * a.max_blocks + x];
+      }
+      to += count;
+    }
+  }
+  sync_all();  // every input of the state has been read, the stack is complete
+  long long from = first + back - 1 - at.need;
+  long long start = at.tokens;
+  for (int i = 0; i < per; ++i) {
+    const int b = lo + i;
+    int len = 0, held = 0, c = 0;
+    bool ignored = false;
+    Sums s{0, 0, 0};
+    if (b < hi) s = plan_request(a, b, len, held, c, ignored);
+    const int count = status == 0 ? static_cast<int>(s.need) : 0;
+    // a few blocks by the request's own thread, many by its warp
+    constexpr int kFew = 4;
+    if (count <= kFew) {
+#pragma unroll
+      for (int x = 0; x < kFew; ++x)
+        if (x < count) a.block_tables[static_cast<int64_t>(b) * a.max_blocks + held + x] = __ldcg(a.free_blocks + from - x);
+    }
+    for (unsigned left = __ballot_sync(kFull, count > kFew); left != 0; left &= left - 1) {
+      const int owner = __ffs(left) - 1;
+      const int cb = __shfl_sync(kFull, b, owner), cn = __shfl_sync(kFull, count, owner), ch = __shfl_sync(kFull, held, owner);
+      const long long cf = __shfl_sync(kFull, from, owner);
+      for (int x = lane; x < cn; x += 32)
+        a.block_tables[static_cast<int64_t>(cb) * a.max_blocks + ch + x] = __ldcg(a.free_blocks + cf - x);
+    }
+    from -= count;
+    if (b < hi) {
+      if constexpr (kRanks == 1) {
+        kept_len[b] = len;
+        kept_count[b] = status == 0 ? static_cast<int>(s.tokens) : 0;
+        kept_start[b] = status == 0 ? static_cast<int>(start) : 0;
+      }
+      if (status == 0) {
+        len = c < 0 ? 0 : len + c;
+        held = c < 0 ? 0 : held + count;
+      }
+      if (a.token_starts != nullptr) a.token_starts[b] = status ? 0 : static_cast<int>(start);
+      start += s.tokens;
+      a.seq_lens_out[b] = len;
+      a.blocks_held_out[b] = held;
+      if (a.appended_out != nullptr) a.appended_out[b] = status ? 0 : static_cast<int>(s.tokens);
+    }
+  }
+  if (rank == 0 && t == 0) {
     if (status != 0) flag_error(a.err, status);
     if (a.status_out != nullptr) *a.status_out = status;
     if (a.token_starts != nullptr) a.token_starts[a.batch] = status ? 0 : static_cast<int>(tokens);
+    *a.num_free_out = status ? first : static_cast<int>(first + back - need);
   }
-  // returned blocks go on the stack before any block is taken from it
-  if (status == 0 && back > 0) {
-    long long to = first + at.back;
-    for (int b = lo; b < hi; ++b)
-      if (a.new_tokens[b] < 0)
-        for (int i = 0; i < a.blocks_held[b]; ++i) a.free_blocks[to++] = a.block_tables[static_cast<size_t>(b) * a.max_blocks + i];
-  }
-  __syncthreads();  // every input of the state has been read, the stack is complete
-  long long from = first + back - 1 - at.need;
-  long long start = at.tokens;
-  for (int b = lo; b < hi; ++b) {
-    int len, held, c;
-    bool ignored = false;
-    const Sums s = plan_request(a, b, len, held, c, ignored);
-    if (status == 0) {
-      for (int i = 0; i < s.need; ++i) a.block_tables[static_cast<size_t>(b) * a.max_blocks + held + i] = a.free_blocks[from--];
-      len = c < 0 ? 0 : len + c;
-      held = c < 0 ? 0 : held + static_cast<int>(s.need);
+  if constexpr (kRanks > 1) cg::this_cluster().sync();  // no CTA leaves while its sums are read
+  if constexpr (kSlots) {
+    __syncthreads();  // tables and lengths are written
+    for (int64_t i = rank * kPlanThreads + t; i < a.num_slots; i += kRanks * kPlanThreads) {
+      int b = 0, off;
+      if (a.max_new > 0) {
+        b = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(a.max_new));
+        off = static_cast<int>(i - static_cast<int64_t>(b) * a.max_new);
+      } else if constexpr (kRanks == 1) {
+        int up = a.batch - 1;  // the largest b that begins at or before i
+        while (b < up) {
+          const int mid = (b + up + 1) >> 1;
+          if (kept_start[mid] <= i) b = mid;
+          else up = mid - 1;
+        }
+        off = static_cast<int>(i - kept_start[b]);
+      } else {
+        off = 0x7fffffff;  // (a large packed call has its own kernel)
+      }
+      int c, base;
+      if constexpr (kRanks == 1) {
+        c = kept_count[b];
+        base = kept_len[b];
+      } else {  // other CTAs wrote it: past the L1 cache
+        c = status == 0 ? a.new_tokens[b] : 0;
+        base = __ldcg(a.seq_lens_out + b) - c;
+      }
+      if (off < c) {
+        write_slot(a, i, b, base, off);
+      } else {
+        a.slots[i] = -1;
+        a.positions[i] = -1;
+      }
     }
-    if (a.token_starts != nullptr) a.token_starts[b] = status ? 0 : static_cast<int>(start);
-    start += s.tokens;
-    a.seq_lens_out[b] = len;
-    a.blocks_held_out[b] = held;
-    if (a.appended_out != nullptr) a.appended_out[b] = status ? 0 : static_cast<int>(s.tokens);
   }
-  if (t == 0) *a.num_free_out = status ? first : static_cast<int>(first + back - need);
-  __syncthreads();
-  // the slots: positions follow from the new length and the count
-  for (int i = t; i < a.num_slots; i += kPlanThreads) {
-    int b = 0, off = 0;
-    bool inside;
-    if (a.max_new > 0) {
-      b = i / a.max_new;
-      off = i - b * a.max_new;
-      inside = off < a.new_tokens[b];
-    } else {
-      inside = i < a.token_starts[a.batch];
-      int up = a.batch - 1;  // the largest b with token_starts[b] <= i
-      while (b < up) {
-        const int mid = (b + up + 1) >> 1;
-        if (a.token_starts[mid] <= i) b = mid;
+}
+
+// The slots of a large packed call, one per thread.  A refused call has no
+// tokens: its starts are all 0.
+constexpr int kSlotThreads = 256;
+
+__global__ void __launch_bounds__(kSlotThreads) plan_slots_kernel(const PlanArgs a) {
+  __shared__ int starts[kSlotThreads + 1];
+  pdl_trigger();
+  pdl_wait();
+  const int t = threadIdx.x, lane = t & 31;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSlotThreads, i = i0 + t;
+  const int tokens = a.token_starts[a.batch];
+  if (i0 >= tokens) {
+    if (i < a.num_slots) {
+      a.slots[i] = -1;
+      a.positions[i] = -1;
+    }
+    return;
+  }
+  // the request of slot i0, the last b with token_starts[b] <= i0: 32 ways at a time
+  int lo = 0, count = a.batch;  // it is in [lo, lo + count)
+  while (count > 1) {
+    const int step = (count + 31) / 32;
+    const int b = lo + lane * step;
+    const unsigned below = __ballot_sync(kFull, lane * step < count && a.token_starts[b] <= i0);
+    const int way = 31 - __clz(below);
+    count = min(step, count - way * step);
+    lo += way * step;
+  }
+  // the starts of the block's requests: at most one begins per slot, apart
+  // from requests without tokens, which are walked over
+  int b = lo, off = static_cast<int>(i - a.token_starts[lo]);
+  for (int base = lo; base < a.batch; base += kSlotThreads) {
+    __syncthreads();
+    for (int x = t; x <= kSlotThreads; x += kSlotThreads) starts[x] = base + x <= a.batch ? a.token_starts[base + x] : 0x7fffffff;
+    __syncthreads();
+    const int n = min(kSlotThreads, a.batch - base);
+    if (starts[0] <= i) {
+      int x = 0, up = n - 1;  // the largest x with starts[x] <= i
+      while (x < up) {
+        const int mid = (x + up + 1) >> 1;
+        if (starts[mid] <= i) x = mid;
         else up = mid - 1;
       }
-      off = i - a.token_starts[b];
+      b = base + x;
+      off = static_cast<int>(i - starts[x]);
     }
-    long long slot = -1;
-    int pos = -1;
-    if (inside && status == 0) {
-      const int base = a.seq_lens_out[b] - a.new_tokens[b];
-      pos = base + off;
-      const int block = a.block_tables[static_cast<size_t>(b) * a.max_blocks + pos / a.block_size];
-      if (static_cast<unsigned>(block) < static_cast<unsigned>(a.num_blocks))
-        slot = static_cast<long long>(block) * a.block_size + pos % a.block_size;
-      else
-        flag_error(a.err, PA_DEVERR_BLOCK_ID);
-      if (a.depths != nullptr) pos = base + a.depths[static_cast<size_t>(b) * a.depths_stride + off];
-    }
-    a.slots[i] = slot;
-    a.positions[i] = pos;
+    if (starts[n] > i0 + kSlotThreads - 1) break;  // uniform
+  }
+  if (i >= a.num_slots) return;
+  if (i < tokens) {
+    write_slot(a, i, b, a.seq_lens_out[b] - a.new_tokens[b], off);
+  } else {
+    a.slots[i] = -1;
+    a.positions[i] = -1;
   }
 }
 
@@ -312,7 +457,29 @@ int pa_plan_append(int32_t* block_tables, const int32_t* blocks_held, int32_t* f
                    depths_stride, slot_mapping, positions,       token_starts, seq_lens_out, blocks_held_out,
                    num_free_out, appended_out, status_out, batch,           max_new_tokens, num_slots, num_blocks, block_size,
                    max_blocks_per_seq, err};
-  PA_CUDA_TRY(launch_pdl(plan_append_kernel, dim3(1), dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream), a));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (num_slots < kPlanSpread && batch < kPlanMany) {
+    PA_CUDA_TRY(launch_pdl(plan_append_kernel<1, true>, dim3(1), dim3(kPlanThreads), 0, st, a));
+    return PA_OK;
+  }
+  const bool wide = max_new_tokens == 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPlanCluster);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPlanCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  PA_CUDA_TRY(wide ? cudaLaunchKernelEx(&cfg, plan_append_kernel<kPlanCluster, false>, a)
+                   : cudaLaunchKernelEx(&cfg, plan_append_kernel<kPlanCluster, true>, a));
+  if (wide && num_slots > 0)
+    PA_CUDA_TRY(launch_pdl(plan_slots_kernel, dim3(static_cast<unsigned>((num_slots + kSlotThreads - 1) / kSlotThreads)),
+                           dim3(kSlotThreads), 0, st, a));
   return PA_OK;
 }
 
