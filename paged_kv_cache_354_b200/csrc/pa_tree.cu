@@ -397,6 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       found[1] = u_begin - lo;
     }
   }
+  // query rows past a row tile's last one are never loaded: as zeros they cost
+  // the tensor cores less power than whatever was there
+  for (int i = threadIdx.x; i < 2 * G::kQBytes / 16; i += kThreads)
+    *reinterpret_cast<uint4*>(smem + G::kQ + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();  // the rings' generic writes above, TMA writes below
   tc::fence_before_sync();
   __syncthreads();
@@ -651,6 +655,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok) {
       ok = enter(pw);
       if (!ok || pw.end) break;
+      // Steps in the middle of a segment, where both products are of whole
+      // tiles that need nothing else: few instructions per step, because this
+      // warp shares its quarter of the SM with softmax warps, and what it
+      // spends between two products the tensor cores wait for
+      if (pw.seg == sw.seg && sw.g == pw.g + 2 && pw.g - pw.g0 >= 2) {
+        const int shift = pw.two ? 1 : 0;
+        const int whole = pw.tail / kTile;                           // whole tiles
+        const int clean = max(0, pw.tail - pw.nodes) / kTile;        // of these, without nodes
+        // PV of steps below `clean`, S two steps later of a whole tile that is not the last
+        int until = min(clean << shift, min((whole << shift) - 2, pw.steps - 3 - shift));
+        until += pw.g0;
+        while (pw.g < until) {
+          const int s = pw.g & 1;
+          const uint32_t kb = k_full(kr.stage), vb = v_full(vr.stage), pb = p_full(s);
+          const bool k_polled = mbar_test_wait(kb, kr.parity);
+          const bool v_there = mbar_test_wait(vb, vr.parity);
+          const bool p_there = mbar_test_wait(pb, (pw.g >> 1) & 1);
+          const uint64_t vd = kVDesc | ((sbase + G::kV + vr.stage * G::kTileBytes) >> 4);
+          const uint64_t kd = kKDesc | ((sbase + G::kK + kr.stage * G::kTileBytes) >> 4);
+          const int qi = qc + (pw.two ? (sw.g - sw.g0) & 1 : 0);
+          const uint64_t qd = kQDesc | ((sbase + G::kQ + (qi & 1) * G::kQBytes) >> 4);
+          const uint32_t p = tmem + G::kS + s * kTile;
+          if (!__all_sync(kFull, v_there && p_there)) {
+            ok = warp_wait(vb, vr.parity) && warp_wait(pb, (pw.g >> 1) & 1);
+            if (!ok) break;
+          }
+          tc::fence_after_sync();
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            tc::mma_ts(lead, tmem + G::kO + s * D, p + 8 * i, vd + ((2 * i * G::kGroupStride) >> 4),
+                       tc::idesc_bf16(kRows, D, false, true), 1u);
+          if (!__all_sync(kFull, k_polled)) {
+            ok = warp_wait(kb, kr.parity);
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const int x = i >> 2, kk = i & 3;
+            tc::mma_ss(lead, p, qd + ((x * G::kQSlab + kk * 32) >> 4), kd + ((x * 1024 + kk * 32) >> 4),
+                       tc::idesc_bf16(kRows, kTile, false, false), i > 0 ? 1u : 0u);
+          }
+          tc::commit_by(lead, s_full(s));
+          tc::commit_by(lead, pv_done(s));
+          if (!pw.two || ((pw.g - pw.g0) & 1)) {
+            tc::commit_by(lead, v_empty(vr.stage));
+            tc::commit_by(lead, k_empty(kr.stage));
+            vr.next();
+            kr.next();
+            ++vc;
+            ++kc;
+          }
+          ++pw.g;
+          ++sw.g;
+        }
+        if (!ok) break;
+      }
       const int local = pw.g - pw.g0;
       const int s = pw.g & 1;
       const int tile = pw.two ? local >> 1 : local;
