@@ -121,19 +121,25 @@ __device__ __forceinline__ int cta_of(int total, int u, int ctas) {
   return c;
 }
 
-// prefix[b] = units per KV head of the requests before b, b in [0, batch].
+// prefix[b] = units per KV head of the requests before b, b in [0, batch).
+// The sum is returned; `uniform`: every request with nodes has as many
+// row-tile pairs as num_nodes has.
 template <int BS>
-__device__ __forceinline__ void unit_prefix(int* prefix, int* sums, const TreeArgs& a, bool report) {
+__device__ __forceinline__ int unit_prefix(int* prefix, int* sums, const TreeArgs& a, bool report, bool& uniform) {
   constexpr int kWarps = kThreads / 32;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   int carry = 0;
+  bool same = true;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     const int b = b0 + t;
     int units = 0;
     if (b < a.batch) {
       int len, n;
       tree_lengths<BS>(a, b, report, len, n);
-      if (n > 0) units = pairs_of(a, n) * (tiles_of(len) + a.extra);
+      if (n > 0) {
+        units = pairs_of(a, n) * (tiles_of(len) + a.extra);
+        same &= pairs_of(a, n) == a.pairs;
+      }
     }
     int incl = units;
 #pragma unroll
@@ -152,10 +158,10 @@ __device__ __forceinline__ void unit_prefix(int* prefix, int* sums, const TreeAr
     }
     if (b < a.batch) prefix[b] = before + incl - units;
     carry = all;
-    __syncthreads();
+    if (b0 + kThreads < a.batch) __syncthreads();
   }
-  if (t == 0) prefix[a.batch] = carry;
-  __syncthreads();
+  uniform = __syncthreads_and(same) != 0;
+  return carry;
 }
 
 // What the merge kernel reads of a CTA (kShare ints): the item that its share
@@ -377,30 +383,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(smem_u32(tmem_slot), G::kTmemCols);
     tc::tmem_relinquish();
   }
+  // query rows past a row tile's last one are never loaded: as zeros they cost
+  // the tensor cores less power than whatever was there
+  for (int i = threadIdx.x; i < 2 * G::kQBytes / 16; i += kThreads)
+    *reinterpret_cast<uint4*>(smem + G::kQ + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   pdl_wait();  // every global access below comes after the previous grid
   pdl_trigger();
 
   // the unit prefix sums, in the still idle rings
   int* prefix = reinterpret_cast<int*>(smem + G::kK);
-  unit_prefix<BS>(prefix, reinterpret_cast<int*>(smem + G::kXch), a, blockIdx.x == 0);
+  bool uniform;
   const int hkv = a.num_kv_heads;
-  const int total = hkv * prefix[a.batch];  // fits: checked on the host
+  const int sum = unit_prefix<BS>(prefix, reinterpret_cast<int*>(smem + G::kXch), a, blockIdx.x == 0, uniform);
+  const int total = hkv * sum;  // fits: checked on the host
   const int ctas = ctas_for(a, total, gridDim.x);
   const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= ctas;
   const int u_begin = idle ? 0 : range_begin(total, blockIdx.x, ctas);
   const int u_end = idle ? 0 : range_begin(total, blockIdx.x + 1, ctas);
+  // The line of units: request, KV head, row-tile pair, tile.  When all
+  // requests have the same number of pairs the pair comes first: the CTAs
+  // that need the same keys and values are then at them at the same time, and
+  // all but one find them in L2 (512 rows per KV head, 32 requests: 370
+  // instead of 659 MB from memory)
+  const int levels = uniform ? a.pairs : 1;
+  const int level = idle ? 0 : u_begin / (total / levels);
+  const int in_level = u_begin - level * (total / levels);
   int* found = reinterpret_cast<int*>(smem + G::kXch) + 64;  // the request of the first unit
   for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-    const int lo = hkv * prefix[b], hi = hkv * prefix[b + 1];
-    if (lo <= u_begin && u_begin < hi) {
+    const int lo = hkv * prefix[b], hi = b + 1 < a.batch ? hkv * prefix[b + 1] : total;
+    if (lo <= in_level * levels && in_level * levels < hi) {
       found[0] = b;
-      found[1] = u_begin - lo;
+      found[1] = in_level - lo / levels;
     }
   }
-  // query rows past a row tile's last one are never loaded: as zeros they cost
-  // the tensor cores less power than whatever was there
-  for (int i = threadIdx.x; i < 2 * G::kQBytes / 16; i += kThreads)
-    *reinterpret_cast<uint4*>(smem + G::kQ + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();  // the rings' generic writes above, TMA writes below
   tc::fence_before_sync();
   __syncthreads();
@@ -429,30 +444,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.pairs = pairs_of(a, it.n);
     };
     auto next_item = [&](Item it) -> Item {  // units are left, so there is one
-      if (++it.rp == it.pairs) {
-        it.rp = 0;
-        if (++it.h == hkv) {
-          it.h = 0;
-          do {
-            ++it.b;
-            load_request(it);
-          } while (it.n == 0);
+      if (levels == 1 && ++it.rp < it.pairs) return it;
+      if (levels == 1) it.rp = 0;
+      if (++it.h < hkv) return it;
+      it.h = 0;
+      do {
+        if (++it.b == a.batch) {
+          it.b = 0;
+          ++it.rp;
         }
-      }
+        load_request(it);
+      } while (it.n == 0);
       return it;
     };
     constexpr int kAhead = 32 / G::kTileBlocks;  // tiles per warp load of table entries
+    // a warp's worth of entries as they are: they are checked when used, a
+    // while after they were asked for
     auto fetch = [&](const Item& it, int tile) -> int {
-      const int e = tile * G::kTileBlocks + lane;
-      int block = 0;
-      if (e * BS < it.len) {
-        block = __ldg(a.block_tables + static_cast<int64_t>(it.b) * a.max_blocks + e);
-        if (static_cast<unsigned>(block) >= static_cast<unsigned>(a.num_blocks)) {
-          flag_error(a.err, PA_DEVERR_BLOCK_ID);
-          block = a.num_blocks;  // past the tensor map: TMA fills with zeros
-        }
-      }
-      return block;
+      const unsigned e = static_cast<unsigned>(tile) * G::kTileBlocks + lane;
+      return e * BS < static_cast<unsigned>(it.len)
+                 ? __ldg(a.block_tables + static_cast<int64_t>(it.b) * a.max_blocks + e)
+                 : 0;
     };
     Item cur{b_first, 0, 0, 0, 0, 0, 0};
     int k = 0, ahead = 0;
@@ -460,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_request(cur);
       const int item = r_first / (cur.tiles + a.extra);
       k = r_first - item * (cur.tiles + a.extra);
-      cur.h = item / cur.pairs;
-      cur.rp = item - cur.h * cur.pairs;
+      cur.h = levels > 1 ? item : item / cur.pairs;
+      cur.rp = levels > 1 ? level : item - cur.h * cur.pairs;
       ahead = fetch(cur, k);
     }
     if (lane == 0) {
@@ -511,6 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < cnt && ok; ++i) {
           if (i % kAhead == 0) {
             entries = ahead;
+            if (static_cast<unsigned>(entries) >= static_cast<unsigned>(a.num_blocks)) {
+              flag_error(a.err, PA_DEVERR_BLOCK_ID);
+              entries = a.num_blocks;  // past the tensor map: TMA fills with zeros
+            }
             if (i + kAhead < cnt) ahead = fetch(cur, k + i + kAhead);
           }
           const int mine = __shfl_sync(kFull, entries, (i % kAhead) * G::kTileBlocks + lane % G::kTileBlocks);
@@ -993,24 +1009,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t out_row = (static_cast<int64_t>(b) * a.nodes + token) * a.num_q_heads + h * a.group + row_head;
         const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + segs[j].slot;
         const int part_row = rt * kRows + row;
-        // 16 columns at a time: code that runs once per segment is short, or
+        // 32 columns at a time: code that runs once per segment is short, or
         // fetching it would take longer than running it
         const int c_begin = two ? 0 : s * (D / 2), c_end = two ? D : (s + 1) * (D / 2);
 #pragma unroll 1
-        for (int col = c_begin; col < c_end; col += 16) {
-          uint32_t own[16], other[16] = {};
+        for (int col = c_begin; col < c_end; col += 32) {
+          uint32_t own[32], other[32] = {};
           __syncwarp();
-          tc::tmem_ld_x16(lanes + G::kO + s * D + col, own);
-          tc::wait_ld_x16(own);
-          if (!two) {
-            tc::tmem_ld_x16(lanes + G::kO + (s ^ 1) * D + col, other);
-            tc::wait_ld_x16(other);
-          }
+          tc::tmem_ld_x32(lanes + G::kO + s * D + col, own);
+          if (!two) tc::tmem_ld_x32(lanes + G::kO + (s ^ 1) * D + col, other);
+          tc::wait_ld_x32(own);
+          tc::wait_ld_x32(other);
           if (!valid) continue;
           // an accumulator whose stream saw nothing of the row is not used
-          float o[16];
+          float o[32];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
+          for (int e = 0; e < 32; ++e)
             o[e] = (keep0 > 0.f ? __uint_as_float(own[e]) * keep0 : 0.f) +
                    (keep1 > 0.f ? __uint_as_float(other[e]) * keep1 : 0.f);
           if (poison) {
@@ -1024,21 +1038,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (static_cast<unsigned>(block) >= static_cast<unsigned>(a.num_blocks)) continue;
               const __nv_bfloat16* v = a.pool + ((static_cast<int64_t>(block) * 2 + 1) * hkv + h) * BS * D + (p % BS) * D + col;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
+              for (int e = 0; e < 32; ++e) {
                 const float x = __bfloat162float(v[e]);
                 o[e] += isfinite(x) ? 0.f : x;
               }
             }
           }
           if (flags & kComplete) {
-            uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-            store_32_bytes(a.out + out_row * D + col, w, a.wide_out);
+            for (int x = 0; x < 2; ++x) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[16 * x + 2 * e] * inv, o[16 * x + 2 * e + 1] * inv);
+              store_32_bytes(a.out + out_row * D + col + 16 * x, w, a.wide_out);
+            }
           } else {
             float4* to = a.part_o + (slot * (D / 4) + col / 4) * (2 * kRows) + part_row;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 8; ++e)
               to[e * (2 * kRows)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
@@ -1290,7 +1307,7 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   a.group = num_q_heads / num_kv_heads;
   a.num_blocks = num_blocks;
   a.max_blocks = max_blocks_per_seq;
-  a.max_seq_len = max_seq_len;
+  a.max_seq_len = std::min(max_seq_len, 0x7fffffff - 4096);  // positions of a tile stay in range
   // smallest normal for 0: masked logits stay -inf, the others vanish
   a.scale_log2 = scale == 0.f ? FLT_MIN : fabsf(scale) * 1.4426950408889634f;
   a.negative = scale < 0.f;

@@ -117,6 +117,20 @@ def test_matches_the_oracle(nodes, hq, hkv, d, bs):
     Case(lens, None, nodes, hq, hkv, d, bs, seed=nodes + hq).check()
 
 
+def test_ragged_batch_of_wide_trees():
+    """Requests of one, several and no row-tile pairs in one batch; the
+    requests of one count alone take the other order of work."""
+    rng = np.random.default_rng(31)
+    counts = np.array([70, 3, 0, 33, 64, 1, 70, 16, 48, 17])
+    lens = counts + rng.integers(0, 700, 10)
+    lens[2] = 0
+    Case(lens, counts, 70, 16, 2, 128, 16, seed=32).check()
+    counts = np.array([70, 0, 65, 70, 0, 66, 68, 70])
+    lens = counts + rng.integers(0, 1500, 8)
+    Case(lens, counts, 70, 16, 2, 128, 32, seed=33).check()
+    Case(lens, counts, 70, 48, 2, 64, 16, seed=34).check()
+
+
 @pytest.mark.parametrize("shared", [False, True])
 def test_ragged_batch(shared):
     rng = np.random.default_rng(1)
