@@ -456,7 +456,8 @@ int pa_plan_append(int32_t* block_tables, const int32_t* blocks_held, int32_t* f
  *                nothing is cached.  One >= max_position flags
  *                PA_DEVERR_POSITION and counts as padding.
  * slot_mapping : device int64 [num_tokens]; negative: not cached.  One
- *                beyond the pool flags PA_DEVERR_SLOT and is skipped.
+ *                beyond the pool flags PA_DEVERR_SLOT and is skipped.  Two
+ *                tokens with one slot: unspecified which one lands.
  * head_dim in {64, 128}; rotary_dim a multiple of 16 up to head_dim, or 0.
  * num_q_heads or num_kv_heads may be 0 (then those pointers are not read).
  * ------------------------------------------------------------------------ */
@@ -487,7 +488,7 @@ int pa_norm_rope_and_cache(pa_bf16* q_out, int64_t q_out_stride, pa_bf16* k_out,
  * rounded to bf16 for the tensor-core product, as in pa_decode.
  *
  * q, out     : bf16 [batch][num_nodes][num_q_heads][head_dim]; out in device
- *              or pinned host memory as for pa_decode
+ *              or pinned host memory as for pa_decode, not overlapping q
  * tree_mask  : device uint32 rows of ceil(num_nodes / 32) words, bit i % 32
  *              of word i / 32 = node i; [batch][num_nodes][words], or with
  *              mask_per_request == 0 one tree [num_nodes][words] for all.

@@ -86,10 +86,11 @@ struct TreeArgs {
 template <int BS>
 __device__ __forceinline__ void tree_lengths(const TreeArgs& a, int b, bool report, int& len, int& n) {
   const int raw = a.seq_lens[b];
+  const int given = a.tree_lens != nullptr ? a.tree_lens[b] : a.nodes;
   const long long cap = min(static_cast<long long>(a.max_blocks) * BS, static_cast<long long>(a.max_seq_len));
   len = static_cast<int>(min(static_cast<long long>(max(raw, 0)), cap));
   if (len != raw && report) flag_error(a.err, PA_DEVERR_SEQ_LEN);
-  n = a.tree_lens != nullptr ? a.tree_lens[b] : a.nodes;
+  n = given;
   if (len == 0) {
     n = 0;
   } else if (n < 0 || n > a.nodes || n > len) {
@@ -1280,6 +1281,9 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(tree_mask, 4) ||
       !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(tree_lens, 4) || !aligned(workspace, 256))
     return fail(PA_ERR_INVALID, "%s: misaligned pointer", who);
+  const uintptr_t bytes = static_cast<uintptr_t>(batch) * num_nodes * num_q_heads * head_dim * sizeof(pa_bf16);
+  const uintptr_t out_at = reinterpret_cast<uintptr_t>(out), q_at = reinterpret_cast<uintptr_t>(q);
+  if (out_at < q_at + bytes && q_at < out_at + bytes) return fail(PA_ERR_INVALID, "%s: out overlaps q", who);
   size_t need = 0;
   rc = pa_decode_tree_workspace_size(batch, num_nodes, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, &need);
   if (rc != PA_OK) return rc;

@@ -271,6 +271,64 @@ def test_bad_lengths_counts_and_blocks_are_flagged():
         assert torch.equal(got[[0, 2]], clean[[0, 2]])
 
 
+@pytest.mark.parametrize("nodes,hq,hkv,d", [(1024, 2, 2, 64), (300, 48, 1, 128), (513, 3, 1, 128)])
+def test_the_largest_trees(nodes, hq, hkv, d):
+    Case([nodes, nodes + 300], [nodes, nodes - 7], nodes, hq, hkv, d, 32, seed=40).check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_position_one_node_one_head(d):
+    Case([1], None, 1, 1, 1, d, 16, seed=41).check()
+    Case([1, 0, 2], [1, 0, 1], 1, 3, 3, d, 16, seed=42).check()
+
+
+def test_scale_zero_gives_the_mean_of_the_attended_values():
+    Case([300, 40], None, 12, 8, 2, 128, 16, seed=43, scale=0.0).check()
+
+
+def test_output_on_a_16_byte_boundary():
+    c = Case([100, 40, 600], None, 6, 8, 2, 128, 16, seed=44)
+    clean = c.run()
+    buffer = torch.full((clean.numel() + 16,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out = buffer[8:-8].view(clean.shape)
+    assert out.data_ptr() % 32 == 16
+    assert torch.equal(c.run(out=out), clean)
+    assert torch.isnan(buffer[:8]).all() and torch.isnan(buffer[-8:]).all()
+
+
+def test_output_over_the_queries_is_refused():
+    c = Case([100], None, 6, 8, 2, 128, 16, seed=45)
+    q, mask = c.q.cuda(), pack(c.sees).cuda()
+    ws = torch.empty(pk.pa_decode_tree_workspace_size(1, 6, 8, 2, 128, 16, 100), dtype=torch.uint8, device="cuda")
+    with pytest.raises(pk.PaError, match="overlaps"):
+        pk.pa_decode_tree(q, q, c.pool.cuda(), mask, torch.as_tensor(c.tables).cuda(), torch.as_tensor(c.lens).cuda(),
+                          100, c.scale, ws)
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, many calls in flight on both."""
+    cases = [Case([3000, 40, 777], None, 9, 16, 2, 128, 16, seed=46), Case([70, 4000], None, 30, 16, 2, 128, 16, seed=47)]
+    clean = [c.run() for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    args, outs = [], []
+    for c in cases:
+        b, nodes, hq, d = c.q.shape
+        max_len = int(c.lens.max())
+        need = pk.pa_decode_tree_workspace_size(b, nodes, hq, 2, d, 16, max_len)
+        args.append((c.q.cuda(), c.pool.cuda(), pack(c.sees).cuda(), torch.as_tensor(c.tables).cuda(),
+                     torch.as_tensor(c.lens).cuda(), max_len, c.scale,
+                     torch.empty(need, dtype=torch.uint8, device="cuda")))
+        outs.append([torch.empty_like(args[-1][0]) for _ in range(10)])
+    torch.cuda.synchronize()
+    for i in range(10):
+        for j in range(2):
+            pk.pa_decode_tree(outs[j][i], *args[j], stream=streams[j])
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert all(torch.equal(o, clean[j]) for o in outs[j])
+    assert pk.pa_device_error() == 0
+
+
 def test_pinned_output_and_refused_pageable_output():
     c = Case([100, 40, 60, 300], None, 6, 8, 2, 128, 16, seed=15)
     clean = c.run()

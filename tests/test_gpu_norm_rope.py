@@ -154,3 +154,27 @@ def test_strides_that_do_not_fit_are_refused():
     odd = torch.zeros((4, 8 * 64 + 4), dtype=torch.bfloat16, device="cuda")[:, :512].unflatten(1, (8, 64))
     with pytest.raises(pk.PaError):
         pk.pa_norm_rope_and_cache(y, odd, y, y, None, None, None, None, k_out=y)
+
+
+def test_queries_alone_and_keys_alone():
+    """No KV heads, or no query heads: the other side is written as usual."""
+    q, k, v, pool, slots, pos, weights = make(23, 6, 2, 64, 16, 10)
+    cs = table(500, 64).cuda()
+    none = torch.empty((23, 0, 64), dtype=torch.bfloat16, device="cuda")
+    g_slots, g_pos = torch.as_tensor(slots).cuda(), torch.as_tensor(pos).int().cuda()
+    q_out = torch.empty_like(q)
+    pk.pa_norm_rope_and_cache(q_out, q, none, None, None, None, g_pos, cs, q_weight=weights[0], eps=EPS, k_out=none)
+    pk.pa_norm_rope_and_cache(none, none, k, v, pool, g_slots, g_pos, cs, k_weight=weights[1], eps=EPS)
+    check(q_out, pool, None, q, k, v, slots, pos, weights, cs, False)
+    assert pk.pa_device_error() == 0
+
+
+def test_many_heads_and_many_tokens():
+    """More rows per token than one thread takes at once, more tokens than
+    the resident blocks take in one round."""
+    q, k, v, pool, slots, pos, weights = make(3000, 128, 16, 64, 32, 11, slab=True)
+    cs = table(500, 64).cuda()
+    q_out = torch.empty((3000, 128, 64), dtype=torch.bfloat16, device="cuda")
+    pk.pa_norm_rope_and_cache(q_out, q, k, v, pool, torch.as_tensor(slots).cuda(), torch.as_tensor(pos).int().cuda(),
+                              cs, *weights, eps=EPS)
+    check(q_out, pool, None, q, k, v, slots, pos, weights, cs, False)

@@ -193,3 +193,65 @@ def test_captured_steps():
         g.replay()
         assert slots.tolist() == [x + [-1] * (4 - len(x)) for x in want[4]]
         s.same(want)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_captured_large_steps(packed):
+    """The launches of a large call, replayed: the in-place state advances."""
+    rng = np.random.default_rng(9)
+    batch, most = 700, 12
+    s = State(rng, batch, 16, 30, 40, batch * 20)
+    counts = [int(x) for x in rng.integers(0, most, batch, endpoint=True)]
+    new = dev(counts)
+    shape = (sum(counts) + 300,) if packed else (batch, most)
+    slots = torch.empty(shape, dtype=torch.int64, device="cuda")
+    positions = torch.empty(shape, dtype=torch.int32, device="cuda")
+    starts = torch.empty(batch + 1, dtype=torch.int32, device="cuda")
+
+    def step():
+        pk.pa_plan_append(s.g_tables, s.g_held, s.g_free, s.g_num, s.g_lens, new, slots, positions, 16,
+                          token_starts=starts)
+
+    step()
+    want = s.want(counts)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        s.tables, s.held, s.free, s.lens = want[:4]
+        want = s.want(counts)
+        g.replay()
+        check_tokens((slots, positions, starts), want, None if packed else most, counts)
+        s.same(want)
+
+
+def test_one_long_prompt_among_empty_requests():
+    """Packed slots whose requests are hundreds of entries apart."""
+    batch = 1500
+    s = State(np.random.default_rng(10), batch, 16, 700, 0, 4000, extra=False)
+    new = [0] * batch
+    new[0], new[700], new[701], new[1499] = 5000, 1, 4100, 3
+    got = call(s, new, None, sum(new) + 1000)
+    want = s.want(new)
+    check_tokens(got, want, None, new)
+    s.same(want)
+
+
+@pytest.mark.parametrize("what", ["blocks", "row"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_refused_large_calls_change_nothing(what, packed):
+    batch, most = 2500, 3
+    s = State(np.random.default_rng(11), batch, 16, 8, 50, 10 if what == "blocks" else batch, extra=False)
+    new = [most] * batch
+    if what == "blocks":
+        s.g_held.zero_()
+        s.g_lens.fill_(15)
+    else:
+        s.g_lens[2400] = 8 * 16
+    before = [t.clone() for t in (s.g_tables, s.g_held, s.g_free, s.g_num, s.g_lens)]
+    pk.pa_device_error(clear=True)
+    slots, positions, starts = call(s, new, None if packed else most, most * batch + 9)
+    assert pk.pa_device_error() == (pk.PA_DEVERR_NO_BLOCKS if what == "blocks" else pk.PA_DEVERR_PLAN)
+    for t, was in zip((s.g_tables, s.g_held, s.g_free, s.g_num, s.g_lens), before):
+        assert torch.equal(t, was)
+    assert (slots == -1).all() and (positions == -1).all() and (starts == 0).all()

@@ -68,7 +68,7 @@ def test_norm_rope_refusals():
     assert rope(q_out=A, q=A, qs=512) == pk.PA_ERR_INVALID and "in place" in message()
 
 
-def tree(out=A, q=A, pool=A, mask=A, per=1, tables=A, lens=A, counts=None, b=2, t=3, hq=8, hkv=2, d=128, bs=16,
+def tree(out=A, q=2 * A, pool=A, mask=A, per=1, tables=A, lens=A, counts=None, b=2, t=3, hq=8, hkv=2, d=128, bs=16,
          blocks=10, width=4, longest=64, ws=A, nbytes=1 << 40):
     return lib.pa_decode_tree(out, q, pool, mask, per, tables, lens, counts, b, t, hq, hkv, d, bs, blocks, width,
                               longest, 0.1, ws, nbytes, None)
@@ -84,6 +84,11 @@ def test_decode_tree_refusals():
         assert tree(**{name: None}) == pk.PA_ERR_INVALID and "NULL" in message(), name
         assert tree(**{name: A + 2}) == pk.PA_ERR_INVALID and "misaligned" in message(), name
     assert tree(nbytes=0) == pk.PA_ERR_INVALID and "workspace" in message()
+    size = 2 * 3 * 8 * 128 * 2  # bytes of q and of out
+    for q in (A, A + 16, A + size - 16, A - size + 16):
+        assert tree(q=q) == pk.PA_ERR_INVALID and "overlaps" in message()
+    for q in (A + size, A - size):
+        assert tree(q=q, nbytes=0) == pk.PA_ERR_INVALID and "workspace" in message()
     size = ctypes.c_size_t()
     assert lib.pa_decode_tree_workspace_size(2, 3, 8, 2, 128, 16, 64, None) == pk.PA_ERR_INVALID
     assert lib.pa_decode_tree_workspace_size(2, 3, 8, 2, 96, 16, 64, ctypes.byref(size)) == pk.PA_ERR_UNSUPPORTED
