@@ -459,7 +459,8 @@ int pa_plan_append(int32_t* block_tables, const int32_t* blocks_held, int32_t* f
  *                beyond the pool flags PA_DEVERR_SLOT and is skipped.  Two
  *                tokens with one slot: unspecified which one lands.
  * head_dim in {64, 128}; rotary_dim a multiple of 16 up to head_dim, or 0.
- * num_q_heads or num_kv_heads may be 0 (then those pointers are not read).
+ * num_q_heads or num_kv_heads may be 0 (then those pointers are not read), at
+ * most 65536 each.
  * ------------------------------------------------------------------------ */
 int pa_norm_rope_and_cache(pa_bf16* q_out, int64_t q_out_stride, pa_bf16* k_out,
                            int64_t k_out_stride, pa_bf16* kv_pool, const pa_bf16* q,
@@ -531,6 +532,9 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool,
  * PA_DEVERR_TREE, a block outside the pool PA_DEVERR_BLOCK_ID: then nothing of
  * that request moves and seq_lens_out[b] = seq_lens[b].  A request with L = 0
  * is empty: nothing moves, nothing is flagged, seq_lens_out[b] = 0.
+ *
+ * Requests are moved at the same time: no two of them share a block that
+ * their trees' positions lie in.
  *
  * path       : device int32 [batch][max_path]; entries from a on are not read
  * tree_lens  : device int32 [batch], or NULL: num_nodes for every request

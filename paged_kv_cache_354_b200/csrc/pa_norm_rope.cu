@@ -226,6 +226,8 @@ extern "C" int pa_norm_rope_and_cache(pa_bf16* q_out, int64_t q_out_stride, pa_b
   const char* who = "pa_norm_rope_and_cache";
   if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0 || num_q_heads + static_cast<int64_t>(num_kv_heads) == 0)
     return fail(PA_ERR_INVALID, "%s: non-positive size", who);
+  if (num_q_heads > 65536 || num_kv_heads > 65536)
+    return fail(PA_ERR_UNSUPPORTED, "%s: %d and %d heads, beyond 65536", who, num_q_heads, num_kv_heads);
   if (head_dim != 64 && head_dim != 128) return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d", who, head_dim);
   if (rotary_dim < 0 || rotary_dim % 16 != 0 || rotary_dim > head_dim)
     return fail(PA_ERR_INVALID, "%s: rotary_dim %d is not a multiple of 16 up to head_dim", who, rotary_dim);

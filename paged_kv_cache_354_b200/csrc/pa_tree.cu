@@ -1097,6 +1097,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kMergeWarps = 8;
 constexpr int kMergeBatch = 4;  // partials in flight
 
+// 2^x, x <= 0, as a partial's weight: never 0, since an infinite value keeps
+// its effect however small the weight is
+__device__ __forceinline__ float weight_of(float x) { return fmaxf(ex2(x), 0x1p-149f); }
+
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeArgs a, int launched) {
   constexpr int kGroups = D / 4 / kMergeWarps;  // column groups per warp
@@ -1144,7 +1148,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
 #pragma unroll
       for (int y = 0; y < kMergeBatch; ++y)
         if (f0 + y < parts) mn = fmaxf(mn, ml[y].x);
-      const float keep = top == -INFINITY ? 0.f : ex2(top - mn);
+      const float keep = top == -INFINITY ? 0.f : weight_of(top - mn);
       l *= keep;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) o[i] = make_float4(o[i].x * keep, o[i].y * keep, o[i].z * keep, o[i].w * keep);
@@ -1153,7 +1157,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
       for (int y = 0; y < kMergeBatch; ++y) {
         // a partial that saw nothing of the row weighs nothing
         if (f0 + y >= parts || (ml[y].x == -INFINITY && ml[y].y == 0.f)) continue;
-        const float w = ex2(ml[y].x - mn);
+        const float w = weight_of(ml[y].x - mn);
         l += ml[y].y * w;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i)

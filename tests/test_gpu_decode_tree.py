@@ -271,6 +271,29 @@ def test_bad_lengths_counts_and_blocks_are_flagged():
         assert torch.equal(got[[0, 2]], clean[[0, 2]])
 
 
+@pytest.mark.parametrize("nodes,hq,d", [(12, 4, 128), (40, 8, 128), (40, 8, 64)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_infinite_value_of_vanishing_weight_in_a_cut_request(nodes, hq, d, value):
+    """A request long enough to be cut between CTAs whose prefix outweighs the
+    tree by more than fp32 can hold: an infinite value under a node still
+    reaches the nodes that attend to it, and only them."""
+    length = 20000
+    c = Case([length], None, nodes, hq, 1, d, 16, seed=50, scale=1.0)
+    c.q.fill_(2.0)
+    block, off = c.slot(0, 5)
+    c.pool[block, 0, 0, off] = 4.0  # a logit of 8 d; the others are within a few times 2 sqrt(d)
+    clean = c.run()
+    block, off = c.slot(0, length - nodes + 3)
+    c.pool[block, 1, 0, off, 7] = value
+    got = c.run()
+    sees = torch.as_tensor(c.sees[0, :, 3])
+    assert sees.any() and not sees.all()
+    hit = got.cpu()[0, sees][..., 7]
+    assert torch.isnan(hit).all() if math.isnan(value) else (hit == math.inf).all()
+    got[0, sees.cuda(), :, 7] = clean[0, sees.cuda(), :, 7]
+    assert torch.equal(got, clean)
+
+
 @pytest.mark.parametrize("nodes,hq,hkv,d", [(1024, 2, 2, 64), (300, 48, 1, 128), (513, 3, 1, 128)])
 def test_the_largest_trees(nodes, hq, hkv, d):
     Case([nodes, nodes + 300], [nodes, nodes - 7], nodes, hq, hkv, d, 32, seed=40).check()

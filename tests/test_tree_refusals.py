@@ -52,7 +52,8 @@ def rope(q_out=A, qos=256, k_out=None, kos=0, pool=A, q=A, qs=256, k=A, ks=128, 
 
 def test_norm_rope_refusals():
     assert rope(n=0) == pk.PA_OK
-    assert rope(d=96) == pk.PA_ERR_UNSUPPORTED
+    for bad in ({"d": 96}, {"hq": 65537}, {"hkv": 65537}):
+        assert rope(**bad) == pk.PA_ERR_UNSUPPORTED, bad
     for bad in ({"n": -1}, {"hq": -1}, {"hkv": -1}, {"hq": 0, "hkv": 0}, {"rot": 8}, {"rot": 72}, {"rot": 80},
                 {"rot": -16}, {"eps": -1.0}, {"eps": float("nan")}, {"most": 0}, {"blocks": 0}, {"bs": 0}):
         assert rope(**bad) == pk.PA_ERR_INVALID, bad
