@@ -561,7 +561,8 @@ def pa_tree_accept(kv_pool, path, accept_lens, block_tables, seq_lens, tree_lens
                 seq_lens=seq_lens, tree_lens=tree_lens, seq_lens_out=seq_lens_out)
     nb, two, hkv, bs, d = kv_pool.shape
     b, most = path.shape
-    if (two != 2 or accept_lens.shape != (b,) or seq_lens.shape != (b,) or block_tables.shape[0] != b
+    if (two != 2 or accept_lens.shape != (b,) or seq_lens.shape != (b,) or block_tables.dim() != 2
+            or block_tables.shape[0] != b
             or (tree_lens is not None and tree_lens.shape != (b,))
             or (seq_lens_out is not None and seq_lens_out.shape != (b,))):
         raise ValueError(f"{where}: shape mismatch")

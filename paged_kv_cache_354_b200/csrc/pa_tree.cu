@@ -122,46 +122,66 @@ __device__ __forceinline__ int cta_of(int total, int u, int ctas) {
   return c;
 }
 
-// prefix[b] = units per KV head of the requests before b, b in [0, batch).
-// The sum is returned; `uniform`: every request with nodes has as many
-// row-tile pairs as num_nodes has.
+// A request in the line of units (per KV head).
+struct InLine {
+  int before, units;  // units of the requests before it, its own
+  int len, n;
+};
+
+// The sum of all requests' units per KV head.  `mine`: request threadIdx.x,
+// when it exists; prefix[b], units of the requests before b, for batches
+// beyond one request per thread (visible after the caller's barrier).
+// `uniform`: every request with nodes has as many row-tile pairs as num_nodes
+// has.
 template <int BS>
-__device__ __forceinline__ int unit_prefix(int* prefix, int* sums, const TreeArgs& a, bool report, bool& uniform) {
+__device__ __forceinline__ int unit_prefix(int* prefix, int* sums, const TreeArgs& a, bool report, bool& uniform,
+                                           InLine& mine) {
   constexpr int kWarps = kThreads / 32;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   int carry = 0;
-  bool same = true;
+  int same = 1;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     const int b = b0 + t;
-    int units = 0;
+    InLine x{0, 0, 0, 0};
+    bool other = false;
     if (b < a.batch) {
-      int len, n;
-      tree_lengths<BS>(a, b, report, len, n);
-      if (n > 0) {
-        units = pairs_of(a, n) * (tiles_of(len) + a.extra);
-        same &= pairs_of(a, n) == a.pairs;
+      tree_lengths<BS>(a, b, report, x.len, x.n);
+      const int pairs = pairs_of(a, x.n);
+      if (x.n > 0) {
+        x.units = pairs * (tiles_of(x.len) + a.extra);
+        other = pairs != a.pairs;
       }
     }
-    int incl = units;
+    int incl = x.units;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(kFull, incl, off);
       if (lane >= off) incl += y;
     }
-    if (lane == 31) sums[warp] = incl;
+    const int warp_same = __all_sync(kFull, !other);
+    if (lane == 31) {
+      sums[warp] = incl;
+      sums[kWarps + warp] = warp_same;
+    }
     __syncthreads();
-    int before = carry, all = carry;
+    int all = carry;
+    x.before = carry;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const int x = sums[w];
-      before += w < warp ? x : 0;
-      all += x;
+      const int y = sums[w];
+      x.before += w < warp ? y : 0;
+      all += y;
+      same &= sums[kWarps + w];
     }
-    if (b < a.batch) prefix[b] = before + incl - units;
+    x.before += incl - x.units;
+    if (b0 == 0) mine = x;
+    if (a.batch > kThreads) {
+      if (b < a.batch) prefix[b] = x.before;
+      __syncthreads();
+    }
     carry = all;
-    if (b0 + kThreads < a.batch) __syncthreads();
   }
-  uniform = __syncthreads_and(same) != 0;
+  uniform = same != 0;
   return carry;
 }
 
@@ -235,6 +255,13 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;"
       : "=l"(reinterpret_cast<uint64_t&>(r))
       : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)), "l"(reinterpret_cast<uint64_t&>(z)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
   return r;
 }
 __device__ __forceinline__ float2 add2(float2 x, float2 y) {
@@ -391,11 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // every global access below comes after the previous grid
   pdl_trigger();
 
-  // the unit prefix sums, in the still idle rings
+  // the unit prefix sums (of a large batch in the still idle rings)
   int* prefix = reinterpret_cast<int*>(smem + G::kK);
   bool uniform;
+  InLine mine{0, 0, 0, 0};
   const int hkv = a.num_kv_heads;
-  const int sum = unit_prefix<BS>(prefix, reinterpret_cast<int*>(smem + G::kXch), a, blockIdx.x == 0, uniform);
+  const int sum = unit_prefix<BS>(prefix, reinterpret_cast<int*>(smem + G::kXch), a, blockIdx.x == 0, uniform, mine);
   const int total = hkv * sum;  // fits: checked on the host
   const int ctas = ctas_for(a, total, gridDim.x);
   const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= ctas;
@@ -410,11 +438,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int level = idle ? 0 : u_begin / (total / levels);
   const int in_level = u_begin - level * (total / levels);
   int* found = reinterpret_cast<int*>(smem + G::kXch) + 64;  // the request of the first unit
-  for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-    const int lo = hkv * prefix[b], hi = b + 1 < a.batch ? hkv * prefix[b + 1] : total;
-    if (lo <= in_level * levels && in_level * levels < hi) {
-      found[0] = b;
-      found[1] = in_level - lo / levels;
+  auto look = [&](int b, const InLine& x) {
+    const int lo = hkv * x.before;
+    if (lo > in_level * levels || in_level * levels >= lo + hkv * x.units) return;
+    found[0] = b;
+    found[1] = in_level - lo / levels;
+    found[2] = x.len;
+    found[3] = x.n;
+  };
+  if (a.batch <= kThreads) {
+    look(threadIdx.x, mine);
+  } else {
+    for (int b = threadIdx.x; b < a.batch; b += kThreads) {
+      const int lo = prefix[b], hi = b + 1 < a.batch ? prefix[b + 1] : sum;
+      InLine x{lo, hi - lo, 0, 0};
+      if (hkv * lo <= in_level * levels && in_level * levels < hkv * hi) tree_lengths<BS>(a, b, false, x.len, x.n);
+      look(b, x);
     }
   }
   fence_proxy_async_smem();  // the rings' generic writes above, TMA writes below
@@ -422,7 +461,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int b_first = idle ? 0 : found[0], r_first = idle ? 0 : found[1];
 
   auto give_up = [&]() {
     flag_error(a.err, PA_DEVERR_WAIT_TIMEOUT);
@@ -467,12 +505,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                  ? __ldg(a.block_tables + static_cast<int64_t>(it.b) * a.max_blocks + e)
                  : 0;
     };
-    Item cur{b_first, 0, 0, 0, 0, 0, 0};
+    Item cur{0, 0, 0, 0, 0, 0, 0};
     int k = 0, ahead = 0;
     if (!idle) {
-      load_request(cur);
-      const int item = r_first / (cur.tiles + a.extra);
-      k = r_first - item * (cur.tiles + a.extra);
+      cur.b = found[0];
+      cur.len = found[2];
+      cur.n = found[3];
+      cur.tiles = tiles_of(cur.len);
+      cur.pairs = pairs_of(a, cur.n);
+      const int item = found[1] / (cur.tiles + a.extra);
+      k = found[1] - item * (cur.tiles + a.extra);
       cur.h = levels > 1 ? item : item / cur.pairs;
       cur.rp = levels > 1 ? level : item - cur.h * cur.pairs;
       ahead = fetch(cur, k);
@@ -497,13 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt = max(0, min(k + span, cur.tiles) - k);  // real tiles
       Item after = cur;
       int after_entries = 0;
-      if (u + span < u_end) {  // the next item's first table entries, a segment ahead
-        after = next_item(cur);
-        after_entries = fetch(after, 0);
-      }
+      const int token0 = cur.rp * 2 * a.tile_tokens;
+      const bool two = cur.n - token0 > a.tile_tokens;
+      const int blocks = (cur.len + BS - 1) / BS;
+      int entries = 0;
       if (cnt > 0) {
-        const int token0 = cur.rp * 2 * a.tile_tokens;
-        const bool two = cur.n - token0 > a.tile_tokens;
         if (lane == 0) {
           volatile Segment& s = segs[seg % G::kSegs];
           s.b = cur.b;
@@ -519,9 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(seg_full(seg % G::kSegs));  // release: the record is visible
         }
         ++seg;
-        const int blocks = (cur.len + BS - 1) / BS;
-        int entries = 0;
-        for (int i = 0; i < cnt && ok; ++i) {
+      }
+      for (int i = 0; i < max(cnt, 1) && ok; ++i) {
+        if (cnt > 0) {
           if (i % kAhead == 0) {
             entries = ahead;
             if (static_cast<unsigned>(entries) >= static_cast<unsigned>(a.num_blocks)) {
@@ -570,6 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_5d(sbase + G::kV + vr.stage * G::kTileBytes + lane * G::kBlockBytes, &kv_map, v_full(vr.stage), 0,
                         0, 0, cur.h * (BS / 8), 2 * mine + 1);
           vr.next();
+        }
+        // the next item and its first table entries: a segment ahead, but
+        // after the first loads of this one
+        if (i == 0 && u + span < u_end) {
+          after = next_item(cur);
+          after_entries = fetch(after, 0);
         }
       }
       first = 0;
@@ -888,21 +934,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;  // kept maximum (log2 units) and sum at it
       bool fresh = true;             // no step of this stream yet
       for (int g = g0 + ((s - g0) & 1); g < g0 + steps; g += 2) {
-        const int tile = tile0 + (two ? (g - g0) >> 1 : g - g0);
+        const int pos0 = (tile0 + (two ? (g - g0) >> 1 : g - g0)) * kTile;
+        const bool open = pos0 + kTile <= base;  // nothing to mask
+        uint32_t bits0 = kFull, bits1 = kFull, bits2 = kFull, bits3 = kFull;
+        if (!open && valid) {  // asked for while S is under way
+          bits0 = attended32(mask_row, pos0, base, n);
+          bits1 = attended32(mask_row, pos0 + 32, base, n);
+          bits2 = attended32(mask_row, pos0 + 64, base, n);
+          bits3 = attended32(mask_row, pos0 + 96, base, n);
+        }
         ok = warp_wait(s_full(s), (g >> 1) & 1);
         if (!ok) break;
         tc::fence_after_sync();
         if (work) {
-          const int pos0 = tile * kTile;
-          const bool open = pos0 + kTile <= base;  // nothing to mask
           const uint32_t sp = lanes + G::kS + s * kTile;
           if (!open || a.negative) {
             // masks and signs are settled in tensor memory, so that the code
             // below, which holds the whole row, is the same for every tile
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              const uint32_t bits = open ? kFull : valid ? attended32(mask_row, pos0 + 32 * c, base, n) : 0u;
-              const uint32_t sign = a.negative ? 0x80000000u : 0u;
+              const uint32_t bits = valid ? bits0 : 0u, sign = a.negative ? 0x80000000u : 0u;
+              bits0 = bits1, bits1 = bits2, bits2 = bits3;
               uint32_t x[32];
               __syncwarp();
               tc::tmem_ld_x32(sp + 32 * c, x);
@@ -1006,7 +1058,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (work) {
         const bool poison = segs[j].poison != 0;
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that attends to nothing gets 0
+        if (flags & kComplete) {
+          const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that attends to nothing gets 0
+          keep0 *= inv;
+          keep1 *= inv;
+        }
+        // an accumulator whose stream saw nothing of the row may hold anything
+        const bool bare = __any_sync(kFull, keep0 == 0.f || (!two && keep1 == 0.f));
         const int64_t out_row = (static_cast<int64_t>(b) * a.nodes + token) * a.num_q_heads + h * a.group + row_head;
         const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + segs[j].slot;
         const int part_row = rt * kRows + row;
@@ -1022,12 +1080,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::wait_ld_x32(own);
           tc::wait_ld_x32(other);
           if (!valid) continue;
-          // an accumulator whose stream saw nothing of the row is not used
+          if (bare) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              own[e] = keep0 == 0.f ? 0u : own[e];
+              other[e] = keep1 == 0.f ? 0u : other[e];
+            }
+          }
           float o[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = (keep0 > 0.f ? __uint_as_float(own[e]) * keep0 : 0.f) +
-                   (keep1 > 0.f ? __uint_as_float(other[e]) * keep1 : 0.f);
+          for (int e = 0; e < 32; e += 2) {
+            float2 x = mul2(make_float2(__uint_as_float(other[e]), __uint_as_float(other[e + 1])), make_float2(keep1, keep1));
+            x = fma2(make_float2(__uint_as_float(own[e]), __uint_as_float(own[e + 1])), make_float2(keep0, keep0), x);
+            o[e] = x.x;
+            o[e + 1] = x.y;
+          }
           if (poison) {
             // values of attended nodes that are not finite
             const int tiles = two ? steps >> 1 : steps;
@@ -1050,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x) {
               uint32_t w[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[16 * x + 2 * e] * inv, o[16 * x + 2 * e + 1] * inv);
+              for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[16 * x + 2 * e], o[16 * x + 2 * e + 1]);
               store_32_bytes(a.out + out_row * D + col + 16 * x, w, a.wide_out);
             }
           } else {
