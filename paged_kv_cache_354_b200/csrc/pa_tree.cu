@@ -20,9 +20,28 @@
 // (m, l, O) are joined at the end of the segment, in tensor memory, where
 // both warpgroups reach both accumulators.
 //
+// The softmax passes over S twice, 64 columns at a time in a rolled loop: the
+// maximum, then the weights.  The issuing warp's code must stay in the
+// instruction cache beside it, and a row held whole in registers left it no
+// room (64 trees of 16: 131 us, in two passes 125; one pass that weighs at the
+// kept maximum and repeats when it rose: 114 where two take 112).
+//
 // The work is split like the balanced decode: all (request, KV head, row-tile
 // pair, tile) units in one line, an equal contiguous share per CTA, items cut
 // between CTAs joined by the merge kernel.
+//
+// Bounds and what it takes (times of the GPU alone; in long runs the power
+// limit lowers the clock and adds the second figure):
+//   64 requests of about 2250 positions, 16 nodes, 32 / 8 heads of 128: 625 MB,
+//     95 us at copy rate; 111 us = 5.6 TB/s (128 us).  Memory, and per item
+//     some 8000 cycles in which both streams end one item and begin the next
+//   4 requests of 32768 positions, 32 nodes: 540 MB, 82 us; 100 us (113 us)
+//   32 requests, 64 nodes, 64 / 8 heads: 155 GFLOP, 94 us; 199 us (209 us).
+//     A tile costs a stream 2230 cycles of softmax (two warps share a quarter's
+//     exponentials), 1024 of products, 600 of hand-over, and the two streams
+//     together keep the tensor cores at 40 %, the exponentials at 41 %
+//   one request, 700 positions, 8 nodes: 13.4 us; start-up, one cold pass
+//     through the code, the merge (4 us)
 //
 // What a node does not attend to may hold anything.  K: a masked logit is
 // replaced by -inf whatever it was.  V: 0 * NaN would reach every row of the
@@ -75,7 +94,7 @@ struct TreeArgs {
   int tile_tokens;    // tokens per row tile
   int pairs;          // row-tile pairs of num_nodes tokens
   int num_blocks, max_blocks, max_seq_len;
-  int extra, min_units;
+  int extra;          // units that the start and end of an item count for
   float scale_log2;   // |scale| * log2(e)
   int negative;       // scale < 0: logits change sign
   int wide_out;       // out is 32-byte aligned
@@ -105,10 +124,8 @@ __device__ __forceinline__ int pairs_of(const TreeArgs& a, int n) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// CTAs that share `total` units: at least min_units each.
-__device__ __forceinline__ int ctas_for(const TreeArgs& a, int total, int ctas) {
-  return max(1, min(ctas, total / a.min_units));
-}
+// CTAs that share `total` units: at least one unit each.
+__device__ __forceinline__ int ctas_for(int total, int ctas) { return max(1, min(ctas, total)); }
 // First unit of CTA c's share, floor(total * c / ctas), without a 64-bit division.
 __device__ __forceinline__ int range_begin(int total, int c, int ctas) {
   const int q = total / ctas;
@@ -425,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hkv = a.num_kv_heads;
   const int sum = unit_prefix<BS>(prefix, reinterpret_cast<int*>(smem + G::kXch), a, blockIdx.x == 0, uniform, mine);
   const int total = hkv * sum;  // fits: checked on the host
-  const int ctas = ctas_for(a, total, gridDim.x);
+  const int ctas = ctas_for(total, gridDim.x);
   const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= ctas;
   const int u_begin = idle ? 0 : range_begin(total, blockIdx.x, ctas);
   const int u_end = idle ? 0 : range_begin(total, blockIdx.x + 1, ctas);
@@ -467,7 +484,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
   };
 
-  if (warp < 4) {
   if (warp == kProducer) {
     // ------------------------------------------------------------ producer
     // walks the CTA's units; real segments are published in a ring of
@@ -834,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_last(s_full(j), (sw.g + 1 - j) >> 1);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 4) {
     // ------------------------------------------------- cleaning value tiles
     // first the rows that have no node: 0.  A request's are one piece of out
     {
@@ -904,10 +920,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) give_up();
     __syncwarp();
-  }
   } else {
     // ------------------------------------------------- softmax and epilogue
-    
     const int s = (warp - 4) >> 2;     // stream
     const int qd = warp & 3;           // TMEM lane quadrant
     const int row = 32 * qd + lane;    // of the row tile
@@ -1160,7 +1174,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partials of items cut between CTAs, in the order of the CTAs.  An
 // item is found by the first CTA that continues it; a block takes 32 rows of
 // it: lane = row, a warp D / 32 column groups of four, so a partial is read
-// 512 bytes at a time; the rows are written out through shared memory.
+// 512 bytes at a time; the rows are written out through shared memory.  Its
+// bytes bound it when many items are cut (32 requests of 512 rows per KV head:
+// 33 MB, 16 us cold, 12 us of a call), else its start: 4 us of a call.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeBatch = 4;  // partials in flight
 
@@ -1180,7 +1196,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
   const int* share = a.shares + c * kShare;
   const int first_tile = share[kShareTile], tiles = share[kShareTiles], total = share[kShareTotal];
   if (first_tile <= 0 || first_tile >= tiles) return;  // it begins with an item, or is idle
-  const int ctas = ctas_for(a, total, launched);
+  const int ctas = ctas_for(total, launched);
   const int u0 = range_begin(total, c, ctas) - first_tile;
   const int before = range_begin(total, c - 1, ctas);
   if (before > u0) return;  // the CTA before continues it already
@@ -1388,8 +1404,9 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   a.negative = scale < 0.f;
   a.tile_tokens = std::min(kRows / a.group, num_nodes);
   a.pairs = (num_nodes + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+  // ending one item and beginning the next takes as long as some tiles (64
+  // trees of 16: 111.2 us with 3, 111.6 with 2, 112.3 with 4, 116.5 with 8)
   a.extra = 3;
-  a.min_units = 1;
   const int64_t longest = std::min(static_cast<int64_t>(max_seq_len), static_cast<int64_t>(max_blocks_per_seq) * block_size);
   if (static_cast<int64_t>(batch) * num_kv_heads * a.pairs > 0x7fffffffll / ((longest + kTile - 1) / kTile + a.extra))
     return fail(PA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 tiles of work at these sizes", who);

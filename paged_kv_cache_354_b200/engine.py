@@ -322,7 +322,8 @@ class PagedTreeCache:
                        self.workspace, tree_lens=self.appended)
 
     def accept(self, path, accept_lens):
-        """Keep ``path[b][:accept_lens[b]]`` of the last step's nodes."""
+        """Keep ``path[b][:accept_lens[b]]`` of the last step's nodes: once per
+        step, before the next ``prefill``, ``step`` or ``release``."""
         pa_tree_accept(self.pool, path, accept_lens, self.tables, self.lens, self.appended, seq_lens_out=self.lens)
 
     def release(self, ended):
