@@ -178,3 +178,37 @@ def test_many_heads_and_many_tokens():
     pk.pa_norm_rope_and_cache(q_out, q, k, v, pool, torch.as_tensor(slots).cuda(), torch.as_tensor(pos).int().cuda(),
                               cs, *weights, eps=EPS)
     check(q_out, pool, None, q, k, v, slots, pos, weights, cs, False)
+
+
+def test_offsets_beyond_two_to_the_31():
+    """Slots in the last blocks of a pool of more than 2^31 elements."""
+    q, k, v, pool, slots, pos, weights = make(40, 8, 8, 128, 16, 12)
+    cs = table(500, 128).cuda()
+    n = pool.shape[0]
+    blocks = (1 << 31) // (2 * 8 * 16 * 128) + n + 1
+    big = torch.zeros((blocks,) + pool.shape[1:], dtype=torch.bfloat16, device="cuda")
+    big[-n:] = 7.5
+    q_out, q_out2 = torch.empty_like(q), torch.empty_like(q)
+    g_slots, g_pos = torch.as_tensor(slots).cuda(), torch.as_tensor(pos).int().cuda()
+    pk.pa_norm_rope_and_cache(q_out, q, k, v, pool, g_slots, g_pos, cs, *weights, eps=EPS)
+    far = torch.where(g_slots < 0, g_slots, g_slots + (blocks - n) * 16)
+    pk.pa_norm_rope_and_cache(q_out2, q, k, v, big, far, g_pos, cs, *weights, eps=EPS)
+    assert torch.equal(big[-n:], pool) and torch.equal(q_out, q_out2)
+    assert not big[:-n].view(torch.int32).any()
+    assert pk.pa_device_error() == 0
+
+
+def test_two_streams_at_once():
+    q, k, v, pool, slots, pos, weights = make(700, 8, 2, 128, 16, 13)
+    cs = table(500, 128).cuda()
+    g_slots, g_pos = torch.as_tensor(slots).cuda(), torch.as_tensor(pos).int().cuda()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    pools, outs = [pool.clone(), pool.clone()], [torch.empty_like(q), torch.empty_like(q)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            pk.pa_norm_rope_and_cache(outs[i], q, k, v, pools[i], g_slots, g_pos, cs, *weights, eps=EPS,
+                                      stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        check(outs[i], pools[i], None, q, k, v, slots, pos, weights, cs, False)

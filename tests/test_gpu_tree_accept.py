@@ -93,3 +93,19 @@ def test_bad_blocks_are_flagged_and_nothing_moves(bad):
     pk.pa_tree_accept(got, i32([[0], [3]]), i32([1, 1]), tables, lens, i32([6, 6]))
     assert pk.pa_device_error() == pk.PA_DEVERR_BLOCK_ID
     assert torch.equal(got.cpu().view(torch.int16), pool.view(torch.int16))
+
+
+def test_offsets_beyond_two_to_the_31():
+    """Requests in the last blocks of a pool of more than 2^31 elements."""
+    pool, _, tables, lens = make([40, 90, 33], 8, 128, 16, 5)
+    n = pool.shape[0]
+    path, accepted, counts = i32([[1, 3, 8], [0, 2, 4], [5, 6, 7]]), i32([3, 3, 2]), i32([9, 9, 9])
+    small = pool.cuda()
+    pk.pa_tree_accept(small, path, accepted, tables, lens, counts)
+    blocks = (1 << 31) // (2 * 8 * 16 * 128) + n + 1
+    big = torch.zeros((blocks,) + tuple(pool.shape[1:]), dtype=torch.bfloat16, device="cuda")
+    big[-n:] = pool.cuda()
+    pk.pa_tree_accept(big, path, accepted, tables + (blocks - n), lens, counts)
+    assert np.array_equal(bits(big[-n:]), bits(small)) and not np.array_equal(bits(small), bits(pool))
+    assert not big[:-n].view(torch.int32).any()
+    assert pk.pa_device_error() == 0

@@ -178,3 +178,40 @@ def test_a_step_without_blocks_changes_nothing():
     assert pk.pa_device_error() == pk.PA_DEVERR_TREE
     loop.same_state()
     assert torch.equal(c.pool.view(torch.int16), before.view(torch.int16))
+
+
+def test_step_on_another_stream():
+    """Every call of a step goes to the current stream: behind a long fill on a
+    stream of its own, nothing else may run ahead of its inputs."""
+    loop = Loop(60, seed=3)
+    c = loop.c
+    loop.prefill([40, 3, 0, 100, 17])
+    counts, sees, depths, qkv = loop.draft()
+    path, accepted = loop.pick(counts, sees)
+    host = [torch.tensor(counts, dtype=torch.int32), pack(sees), torch.as_tensor(depths, dtype=torch.int32),
+            torch.as_tensor(path), torch.tensor(accepted, dtype=torch.int32)]
+    given = [t.cuda() for t in host]
+    late = [torch.zeros_like(t) for t in given]
+    out = torch.full((B, T, HQ, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    filler = torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    before = c.pool.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(5):
+            filler.fill_(1)
+        for dst, src in zip(late, given):
+            dst.copy_(src)
+        c.step(*qkv, *late[:3], out)
+        between = c.pool.clone()
+        c.accept(*late[3:])
+    side.synchronize()
+    base = list(loop.state[3])
+    *loop.state, slots, _ = ots.plan_append(*loop.state, counts, BS, WIDTH)
+    flat = np.array([r + [-1] * (T - len(r)) for r in slots]).reshape(-1)
+    positions = np.array([[base[b] + depths[b, t] if t < counts[b] else -1 for t in range(T)] for b in range(B)])
+    after, c.pool = c.pool, between
+    loop.rows_are_cached(qkv[1], qkv[2], positions.reshape(-1), flat, before)
+    c.pool = after
+    loop.check_accept(path, accepted, counts, between)
+    assert torch.isfinite(out).all() and out.any() and pk.pa_device_error() == 0
