@@ -93,6 +93,7 @@ struct TreeArgs {
   int batch, nodes, words, num_q_heads, num_kv_heads, group;
   int tile_tokens;    // tokens per row tile
   int pairs;          // row-tile pairs of num_nodes tokens
+  int pair_factor;    // (x * pair_factor) >> 20 = x / (2 * tile_tokens) for x < 2048
   int num_blocks, max_blocks, max_seq_len;
   int extra;          // units that the start and end of an item count for
   float scale_log2;   // |scale| * log2(e)
@@ -120,24 +121,25 @@ __device__ __forceinline__ void tree_lengths(const TreeArgs& a, int b, bool repo
 
 // Row-tile pairs and tiles of a request; both 0 without nodes.
 __device__ __forceinline__ int pairs_of(const TreeArgs& a, int n) {
-  return (n + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+  return ((n + 2 * a.tile_tokens - 1) * a.pair_factor) >> 20;
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// CTAs that share `total` units: at least one unit each.
-__device__ __forceinline__ int ctas_for(int total, int ctas) { return max(1, min(ctas, total)); }
-// First unit of CTA c's share, floor(total * c / ctas), without a 64-bit division.
-__device__ __forceinline__ int range_begin(int total, int c, int ctas) {
-  const int q = total / ctas;
-  return q * c + (total - q * ctas) * c / ctas;
-}
-// The CTA whose share holds unit u: one guess, then at most a step or two.
-__device__ __forceinline__ int cta_of(int total, int u, int ctas) {
-  int c = min(ctas - 1, static_cast<int>(static_cast<float>(u) * static_cast<float>(ctas) / static_cast<float>(total)));
-  while (range_begin(total, c, ctas) > u) --c;
-  while (c + 1 < ctas && range_begin(total, c + 1, ctas) <= u) ++c;
-  return c;
-}
+// Equal shares of the line of units: the first `more` CTAs get one above
+// `each`.  Every CTA that takes part gets at least one unit.
+struct Split {
+  int ctas, each, more;
+  __device__ __forceinline__ Split(int total, int launched) {
+    ctas = max(1, min(launched, total));
+    each = total / ctas;
+    more = total - each * ctas;
+  }
+  __device__ __forceinline__ int begin(int c) const { return each * c + min(c, more); }
+  __device__ __forceinline__ int holder(int u) const {  // the CTA whose share holds unit u
+    const int high = more * (each + 1);
+    return u < high ? u / (each + 1) : more + (u - high) / each;
+  }
+};
 
 // A request in the line of units (per KV head).
 struct InLine {
@@ -181,16 +183,11 @@ __device__ __forceinline__ int unit_prefix(int* prefix, int* sums, const TreeArg
       sums[kWarps + warp] = warp_same;
     }
     __syncthreads();
-    int all = carry;
-    x.before = carry;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int y = sums[w];
-      x.before += w < warp ? y : 0;
-      all += y;
-      same &= sums[kWarps + w];
-    }
-    x.before += incl - x.units;
+    const int of_warp = lane < kWarps ? sums[lane] : 0;
+    const int same_warp = lane < kWarps ? sums[kWarps + lane] : 1;
+    const int all = carry + __reduce_add_sync(kFull, of_warp);
+    x.before = carry + __reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - x.units;
+    same &= __all_sync(kFull, same_warp);
     if (b0 == 0) mine = x;
     if (a.batch > kThreads) {
       if (b < a.batch) prefix[b] = x.before;
@@ -442,24 +439,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hkv = a.num_kv_heads;
   const int sum = unit_prefix<BS>(prefix, reinterpret_cast<int*>(smem + G::kXch), a, blockIdx.x == 0, uniform, mine);
   const int total = hkv * sum;  // fits: checked on the host
-  const int ctas = ctas_for(total, gridDim.x);
-  const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= ctas;
-  const int u_begin = idle ? 0 : range_begin(total, blockIdx.x, ctas);
-  const int u_end = idle ? 0 : range_begin(total, blockIdx.x + 1, ctas);
+  const Split split(total, gridDim.x);
+  const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= split.ctas;
+  const int u_begin = idle ? 0 : split.begin(blockIdx.x);
+  const int u_end = idle ? 0 : split.begin(blockIdx.x + 1);
   // The line of units: request, KV head, row-tile pair, tile.  When all
   // requests have the same number of pairs the pair comes first: the CTAs
   // that need the same keys and values are then at them at the same time, and
   // all but one find them in L2 (512 rows per KV head, 32 requests: 370
   // instead of 659 MB from memory)
   const int levels = uniform ? a.pairs : 1;
-  const int level = idle ? 0 : u_begin / (total / levels);
-  const int in_level = u_begin - level * (total / levels);
+  int level = 0, in_level = u_begin;
+  if (levels > 1) {
+    level = u_begin / (total / levels);
+    in_level -= level * (total / levels);
+  }
   int* found = reinterpret_cast<int*>(smem + G::kXch) + 64;  // the request of the first unit
   auto look = [&](int b, const InLine& x) {
     const int lo = hkv * x.before;
     if (lo > in_level * levels || in_level * levels >= lo + hkv * x.units) return;
     found[0] = b;
-    found[1] = in_level - lo / levels;
+    found[1] = levels > 1 ? in_level - lo / levels : in_level - lo;
     found[2] = x.len;
     found[3] = x.n;
   };
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cur.pairs = pairs_of(a, cur.n);
       const int item = found[1] / (cur.tiles + a.extra);
       k = found[1] - item * (cur.tiles + a.extra);
-      cur.h = levels > 1 ? item : item / cur.pairs;
+      cur.h = levels > 1 || cur.pairs == 1 ? item : item / cur.pairs;
       cur.rp = levels > 1 ? level : item - cur.h * cur.pairs;
       ahead = fetch(cur, k);
     }
@@ -1196,12 +1196,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
   const int* share = a.shares + c * kShare;
   const int first_tile = share[kShareTile], tiles = share[kShareTiles], total = share[kShareTotal];
   if (first_tile <= 0 || first_tile >= tiles) return;  // it begins with an item, or is idle
-  const int ctas = ctas_for(total, launched);
-  const int u0 = range_begin(total, c, ctas) - first_tile;
-  const int before = range_begin(total, c - 1, ctas);
+  const Split split(total, launched);
+  const int u0 = split.begin(c) - first_tile;
+  const int before = split.begin(c - 1);
   if (before > u0) return;  // the CTA before continues it already
   const int c0 = c - 1;
-  const int parts = cta_of(total, u0 + tiles - 1, ctas) - c0 + 1;
+  const int parts = split.holder(u0 + tiles - 1) - c0 + 1;
   const int b = share[kShareB], h = share[kShareH], n = share[kShareNodes];
   const int rt = blockIdx.y / (kRows / 32);
   const int token0 = (share[kSharePair] * 2 + rt) * a.tile_tokens;
@@ -1404,6 +1404,8 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   a.negative = scale < 0.f;
   a.tile_tokens = std::min(kRows / a.group, num_nodes);
   a.pairs = (num_nodes + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+  // exact: the factor is above 2^20 / d by less than 1, x d <= 1279 * 256 < 2^20
+  a.pair_factor = ((1 << 20) + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
   // ending one item and beginning the next takes as long as some tiles (64
   // trees of 16: 111.2 us with 3, 111.6 with 2, 112.3 with 4, 116.5 with 8)
   a.extra = 3;
