@@ -10,7 +10,7 @@
 // kPlanMany requests on a cluster of 8 shares the requests and exchanges its
 // sums through distributed shared memory, and a packed call of that size
 // leaves its slots to a second, wide launch (1000 requests, 256k slots: 328 us
-// on one CTA, 66 us when the cluster wrote the slots, 18 us so; floor 0.6 us).
+// on one CTA, 66 us when the cluster wrote the slots, 16.8 us so; floor 0.6 us).
 //
 // pa_tree_accept moves rows of the pool.  A thread owns one 16-byte column of
 // the rows of one request and walks the path in order: step i writes row i
@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_append_kernel(const PlanArg
   namespace cg = cooperative_groups;
   __shared__ long long part[3][32];
   __shared__ long long mine_total[4];  // of this CTA: back, need, tokens, bad
+  __shared__ long long totals[kRanks][4];
   // a single CTA keeps what its slots follow from
   constexpr int kKept = kRanks == 1 ? kPlanMany : 1;
   __shared__ int kept_len[kKept], kept_count[kKept], kept_start[kKept];
@@ -159,11 +160,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_append_kernel(const PlanArg
     at.need += part[1][warp - 1];
     at.tokens += part[2][warp - 1];
   }
+  if constexpr (kRanks > 1) {  // one remote load per CTA and sum (one per thread: 18.0 us, so 16.8)
+    if (t < 4 * kRanks) totals[t >> 2][t & 3] = cg::this_cluster().map_shared_rank(mine_total, t >> 2)[t & 3];
+    __syncthreads();
+  }
   long long back = 0, need = 0, tokens = 0, wrong = 0;
 #pragma unroll
   for (int r = 0; r < kRanks; ++r) {
-    const long long* other = mine_total;
-    if constexpr (kRanks > 1) other = cg::this_cluster().map_shared_rank(mine_total, r);
+    const long long* other = kRanks > 1 ? totals[r] : mine_total;
     if (r < rank) {
       at.back += other[0];
       at.need += other[1];
