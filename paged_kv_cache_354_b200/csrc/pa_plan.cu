@@ -89,6 +89,35 @@ __device__ __forceinline__ long long warp_inclusive(long long v, int lane) {
   return v;
 }
 
+// Every lane's run of `count` entries, from src on upwards (dir 1) or downwards
+// (-1), to dst on: the runs of a warp in one line, kRunDepth entries per lane
+// in flight, since a run after the other waits for memory once per run.
+constexpr int kRunDepth = 4;
+
+__device__ __forceinline__ void copy_runs(int count, const int32_t* src, int dir, int32_t* dst, int lane) {
+  const unsigned incl = static_cast<unsigned>(warp_inclusive(count, lane));  // at most num_blocks in all
+  const unsigned total = __shfl_sync(kFull, incl, 31);
+  for (unsigned e0 = lane; e0 - lane < total; e0 += 32 * kRunDepth) {
+    int32_t v[kRunDepth];
+    int32_t* to[kRunDepth];
+#pragma unroll
+    for (int u = 0; u < kRunDepth; ++u) {
+      const unsigned e = e0 + 32 * u;
+      int owner = 0;  // the first lane whose run ends beyond e
+#pragma unroll
+      for (int step = 16; step >= 1; step >>= 1)
+        if (__shfl_sync(kFull, incl, owner + step - 1) <= e) owner += step;
+      const int x = static_cast<int>(e - (__shfl_sync(kFull, incl, owner) - __shfl_sync(kFull, count, owner)));
+      const int32_t* from = reinterpret_cast<const int32_t*>(__shfl_sync(kFull, reinterpret_cast<uintptr_t>(src), owner));
+      to[u] = reinterpret_cast<int32_t*>(__shfl_sync(kFull, reinterpret_cast<uintptr_t>(dst), owner)) + x;
+      v[u] = e < total ? __ldcg(from + static_cast<int64_t>(dir) * x) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kRunDepth; ++u)
+      if (e0 + 32 * u < total) *to[u] = v[u];
+  }
+}
+
 // Entry of a slot: position p of a request whose tokens begin at `base`.
 __device__ __forceinline__ void write_slot(const PlanArgs& a, int64_t i, int b, int base, int off) {
   const int p = base + off;
@@ -181,19 +210,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_append_kernel(const PlanArg
   int status = 0;
   if (wrong || first < 0 || first + back > a.num_blocks || tokens > a.num_slots) status = PA_DEVERR_PLAN;
   else if (need > first + back) status = PA_DEVERR_NO_BLOCKS;
-  // returned blocks go on the stack before any block is taken from it; a
-  // warp copies its requests' blocks one request after the other
+  // returned blocks go on the stack before any block is taken from it
   if (status == 0 && back > 0) {
     long long to = first + at.back;
     for (int i = 0; i < per; ++i) {
       const int b = lo + i;
       const int count = b < hi && a.new_tokens[b] < 0 ? a.blocks_held[b] : 0;
-      for (unsigned left = __ballot_sync(kFull, count > 0); left != 0; left &= left - 1) {
-        const int from = __ffs(left) - 1;
-        const int cb = __shfl_sync(kFull, b, from), cn = __shfl_sync(kFull, count, from);
-        const long long ct = __shfl_sync(kFull, to, from);
-        for (int x = lane; x < cn; x += 32) a.free_blocks[ct + x] = a.block_tables[static_cast<int64_t>(cb) * a.max_blocks + x];
-      }
+      copy_runs(count, a.block_tables + static_cast<int64_t>(b) * a.max_blocks, 1, a.free_blocks + to, lane);
       to += count;
     }
   }
@@ -207,20 +230,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_append_kernel(const PlanArg
     Sums s{0, 0, 0};
     if (b < hi) s = plan_request(a, b, len, held, c, ignored);
     const int count = status == 0 ? static_cast<int>(s.need) : 0;
-    // a few blocks by the request's own thread, many by its warp
+    // a few blocks by the request's own thread (a step's), many by its warp
     constexpr int kFew = 4;
     if (count <= kFew) {
 #pragma unroll
       for (int x = 0; x < kFew; ++x)
         if (x < count) a.block_tables[static_cast<int64_t>(b) * a.max_blocks + held + x] = __ldcg(a.free_blocks + from - x);
     }
-    for (unsigned left = __ballot_sync(kFull, count > kFew); left != 0; left &= left - 1) {
-      const int owner = __ffs(left) - 1;
-      const int cb = __shfl_sync(kFull, b, owner), cn = __shfl_sync(kFull, count, owner), ch = __shfl_sync(kFull, held, owner);
-      const long long cf = __shfl_sync(kFull, from, owner);
-      for (int x = lane; x < cn; x += 32)
-        a.block_tables[static_cast<int64_t>(cb) * a.max_blocks + ch + x] = __ldcg(a.free_blocks + cf - x);
-    }
+    copy_runs(count > kFew ? count : 0, a.free_blocks + from, -1,
+              a.block_tables + static_cast<int64_t>(b) * a.max_blocks + held, lane);
     from -= count;
     if (b < hi) {
       if constexpr (kRanks == 1) {
