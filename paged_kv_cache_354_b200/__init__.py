@@ -365,16 +365,17 @@ def _refuse(where, dtype, device, **tensors):
                 raise ValueError(f"{where}: {name} is on cuda:{t.get_device()}, other tensors on cuda:{device}")
 
 
-def _launch(where, device, stream, fn, *args):
-    """Call fn(*args, stream) with ``device`` current."""
-    import torch
+def _raw_stream(torch, device, stream):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
-    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+def _launch(torch, where, device, fn, args):
+    """Call fn(*args) with ``device`` current."""
     if device == torch._C._cuda_getDevice():
-        status = fn(*args, raw)
+        status = fn(*args)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, raw)
+            status = fn(*args)
     if status != PA_OK:
         _check(status, where)
 
@@ -429,10 +430,12 @@ def pa_plan_append(block_tables, blocks_held, free_blocks, num_free, seq_lens, n
         if not padded or depths.shape not in ((most,), (b, most)):
             raise ValueError(f"{where}: shape mismatch")
         stride = most if depths.dim() == 2 else 0
-    _launch(where, device, stream, lib.pa_plan_append, _adr(block_tables), _adr(blocks_held), _adr(free_blocks),
-            _adr(num_free), _adr(seq_lens), _adr(new_tokens), _adr(depths), stride, _adr(slot_mapping),
-            _adr(positions), _adr(token_starts), _adr(seq_lens_out), _adr(blocks_held_out), _adr(num_free_out),
-            _adr(appended_out), _adr(status_out), b, most, slot_mapping.numel(), free_blocks.shape[0], int(block_size), width)
+    _launch(torch, where, device, lib.pa_plan_append,
+            (block_tables.data_ptr(), blocks_held.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
+             seq_lens.data_ptr(), new_tokens.data_ptr(), _adr(depths), stride, slot_mapping.data_ptr(),
+             positions.data_ptr(), _adr(token_starts), seq_lens_out.data_ptr(), blocks_held_out.data_ptr(),
+             num_free_out.data_ptr(), _adr(appended_out), _adr(status_out), b, most, slot_mapping.numel(),
+             free_blocks.shape[0], int(block_size), width, _raw_stream(torch, device, stream)))
 
 
 def _token_rows(where, device, dtype, name, t, shape):
@@ -500,9 +503,11 @@ def pa_norm_rope_and_cache(q_out, q, k, v, kv_pool, slot_mapping, positions, cos
             _refuse(where, bf16, device, q_weight=q_weight, k_weight=k_weight)
         if (q_weight is not None and q_weight.shape != (d,)) or (k_weight is not None and k_weight.shape != (d,)):
             raise ValueError(f"{where}: shape mismatch")
-    _launch(where, device, stream, lib.pa_norm_rope_and_cache, _adr(q_out), qos, _adr(k_out), kos, _adr(kv_pool),
-            _adr(q), qs, _adr(k), ks, _adr(v), vs, _adr(q_weight), _adr(k_weight), eps, _adr(cos_sin), most, rotary,
-            1 if interleaved else 0, _adr(positions), _adr(slot_mapping), n, hq, hkv, d, blocks, block_size)
+    _launch(torch, where, device, lib.pa_norm_rope_and_cache,
+            (q_out.data_ptr(), qos, _adr(k_out), kos, _adr(kv_pool), q.data_ptr(), qs, k.data_ptr(), ks, _adr(v), vs,
+             _adr(q_weight), _adr(k_weight), eps, _adr(cos_sin), most, rotary, 1 if interleaved else 0,
+             _adr(positions), _adr(slot_mapping), n, hq, hkv, d, blocks, block_size,
+             _raw_stream(torch, device, stream)))
 
 
 def pa_decode_tree_workspace_size(batch, num_nodes, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len):
@@ -538,9 +543,11 @@ def pa_decode_tree(out, q, kv_pool, tree_mask, block_tables, seq_lens, max_seq_l
             or seq_lens.shape != (b,) or (tree_lens is not None and tree_lens.shape != (b,))
             or tree_mask.shape not in (rows, (b,) + rows)):
         raise ValueError(f"{where}: shape mismatch")
-    _launch(where, device, stream, lib.pa_decode_tree, _adr(out), _adr(q), _adr(kv_pool), _adr(tree_mask),
-            1 if tree_mask.dim() == 3 else 0, _adr(block_tables), _adr(seq_lens), _adr(tree_lens), b, t, hq, hkv, d,
-            bs, nb, block_tables.shape[1], int(max_seq_len), float(scale), _adr(workspace), workspace.numel())
+    _launch(torch, where, device, lib.pa_decode_tree,
+            (out.data_ptr(), q.data_ptr(), kv_pool.data_ptr(), tree_mask.data_ptr(), 1 if tree_mask.dim() == 3 else 0,
+             block_tables.data_ptr(), seq_lens.data_ptr(), _adr(tree_lens), b, t, hq, hkv, d, bs, nb,
+             block_tables.shape[1], int(max_seq_len), float(scale), workspace.data_ptr(), workspace.numel(),
+             _raw_stream(torch, device, stream)))
 
 
 def pa_tree_accept(kv_pool, path, accept_lens, block_tables, seq_lens, tree_lens, seq_lens_out=None, num_nodes=None,
@@ -569,9 +576,10 @@ def pa_tree_accept(kv_pool, path, accept_lens, block_tables, seq_lens, tree_lens
     if tree_lens is None and num_nodes is None:
         raise ValueError(f"{where}: tree_lens or num_nodes")
     nodes = 0x7fffffff if num_nodes is None else int(num_nodes)
-    _launch(where, device, stream, lib.pa_tree_accept, _adr(kv_pool), _adr(path), _adr(accept_lens), _adr(tree_lens),
-            _adr(block_tables), _adr(seq_lens), _adr(seq_lens_out), b, nodes, most, nb, hkv, bs, d,
-            block_tables.shape[1])
+    _launch(torch, where, device, lib.pa_tree_accept,
+            (kv_pool.data_ptr(), path.data_ptr(), accept_lens.data_ptr(), _adr(tree_lens), block_tables.data_ptr(),
+             seq_lens.data_ptr(), _adr(seq_lens_out), b, nodes, most, nb, hkv, bs, d, block_tables.shape[1],
+             _raw_stream(torch, device, stream)))
 
 
 def pa_selftest_wait_timeout(limit_ns, stream=None):
