@@ -33,14 +33,14 @@
 // Bounds and what it takes (times of the GPU alone; in long runs the power
 // limit lowers the clock and adds the second figure):
 //   64 requests of about 2250 positions, 16 nodes, 32 / 8 heads of 128: 625 MB,
-//     95 us at copy rate; 111 us = 5.6 TB/s (128 us).  Memory, and per item
+//     95 us at copy rate; 110 us = 5.7 TB/s (129 us).  Memory, and per item
 //     some 8000 cycles in which both streams end one item and begin the next
-//   4 requests of 32768 positions, 32 nodes: 540 MB, 82 us; 100 us (113 us)
-//   32 requests, 64 nodes, 64 / 8 heads: 155 GFLOP, 94 us; 199 us (209 us).
-//     A tile costs a stream 2230 cycles of softmax (two warps share a quarter's
-//     exponentials), 1024 of products, 600 of hand-over, and the two streams
-//     together keep the tensor cores at 40 %, the exponentials at 41 %
-//   one request, 700 positions, 8 nodes: 13.4 us; start-up, one cold pass
+//   4 requests of 32768 positions, 32 nodes: 540 MB, 82 us; 99 us (115 us)
+//   32 requests, 64 nodes, 64 / 8 heads: 155 GFLOP, 94 us; 190 to 203 us
+//     (214 us).  A tile costs a stream 2230 cycles of softmax (two warps share
+//     a quarter's exponentials), 1024 of products and 600 of hand-over; the two
+//     streams keep the tensor cores at 40 %, the exponentials at 41 %
+//   one request, 700 positions, 8 nodes: 12.4 us; start-up, one cold pass
 //     through the code, the merge (4 us)
 //
 // What a node does not attend to may hold anything.  K: a masked logit is
