@@ -93,6 +93,7 @@ struct TreeArgs {
   int batch, nodes, words, num_q_heads, num_kv_heads, group;
   int tile_tokens;    // tokens per row tile
   int pairs;          // row-tile pairs of num_nodes tokens
+  unsigned cta_factor;  // __umulhi(x, cta_factor) = x / CTAs launched for x < CTAs^2
   int pair_factor;    // (x * pair_factor) >> 20 = x / (2 * tile_tokens) for x < 2048
   int num_blocks, max_blocks, max_seq_len;
   int extra;          // units that the start and end of an item count for
@@ -125,19 +126,23 @@ __device__ __forceinline__ int pairs_of(const TreeArgs& a, int n) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// Equal shares of the line of units: the first `more` CTAs get one above
-// `each`.  Every CTA that takes part gets at least one unit.
+// Equal shares of the line of units, at least a unit each: CTA c begins at
+// floor(total c / ctas).  What is left over is spread evenly, so that the CTAs
+// half a line apart stay together over the whole line (see `levels`).
 struct Split {
-  int ctas, each, more;
-  __device__ __forceinline__ Split(int total, int launched) {
+  int total, ctas, each;
+  unsigned more, factor;
+  __device__ __forceinline__ Split(int total, int launched, unsigned factor) : total(total), factor(factor) {
     ctas = max(1, min(launched, total));
     each = total / ctas;
-    more = total - each * ctas;
+    more = total - each * ctas;  // 0 unless every launched CTA takes part
   }
-  __device__ __forceinline__ int begin(int c) const { return each * c + min(c, more); }
-  __device__ __forceinline__ int holder(int u) const {  // the CTA whose share holds unit u
-    const int high = more * (each + 1);
-    return u < high ? u / (each + 1) : more + (u - high) / each;
+  __device__ __forceinline__ int begin(int c) const { return each * c + static_cast<int>(__umulhi(more * c, factor)); }
+  __device__ __forceinline__ int holder(int u) const {  // the CTA whose share holds unit u: a guess, then a step or two
+    int c = min(ctas - 1, static_cast<int>(static_cast<float>(u) * static_cast<float>(ctas) / static_cast<float>(total)));
+    while (begin(c) > u) --c;
+    while (c + 1 < ctas && begin(c + 1) <= u) ++c;
+    return c;
   }
 };
 
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hkv = a.num_kv_heads;
   const int sum = unit_prefix<BS>(prefix, reinterpret_cast<int*>(smem + G::kXch), a, blockIdx.x == 0, uniform, mine);
   const int total = hkv * sum;  // fits: checked on the host
-  const Split split(total, gridDim.x);
+  const Split split(total, gridDim.x, a.cta_factor);
   const bool idle = total == 0 || static_cast<int>(blockIdx.x) >= split.ctas;
   const int u_begin = idle ? 0 : split.begin(blockIdx.x);
   const int u_end = idle ? 0 : split.begin(blockIdx.x + 1);
@@ -1196,7 +1201,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
   const int* share = a.shares + c * kShare;
   const int first_tile = share[kShareTile], tiles = share[kShareTiles], total = share[kShareTotal];
   if (first_tile <= 0 || first_tile >= tiles) return;  // it begins with an item, or is idle
-  const Split split(total, launched);
+  const Split split(total, launched, a.cta_factor);
   const int u0 = split.begin(c) - first_tile;
   const int before = split.begin(c - 1);
   if (before > u0) return;  // the CTA before continues it already
@@ -1409,6 +1414,8 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   // ending one item and beginning the next takes as long as some tiles (64
   // trees of 16: 111.2 us with 3, 111.6 with 2, 112.3 with 4, 116.5 with 8)
   a.extra = 3;
+  const unsigned ctas = std::max(sm_count(), 1);
+  a.cta_factor = ctas > 1 ? 0xffffffffu / ctas + 1 : 0;  // exact: x ctas < ctas^3 < 2^32
   const int64_t longest = std::min(static_cast<int64_t>(max_seq_len), static_cast<int64_t>(max_blocks_per_seq) * block_size);
   if (static_cast<int64_t>(batch) * num_kv_heads * a.pairs > 0x7fffffffll / ((longest + kTile - 1) / kTile + a.extra))
     return fail(PA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 tiles of work at these sizes", who);
