@@ -33,11 +33,11 @@
 // Bounds and what it takes (times of the GPU alone; in long runs the power
 // limit lowers the clock and adds the second figure):
 //   64 requests of about 2250 positions, 16 nodes, 32 / 8 heads of 128: 625 MB,
-//     95 us at copy rate; 110 us = 5.7 TB/s (129 us).  Memory, and per item
+//     95 us at copy rate; 111 us = 5.6 TB/s (129 us).  Memory, and per item
 //     some 8000 cycles in which both streams end one item and begin the next
-//   4 requests of 32768 positions, 32 nodes: 540 MB, 82 us; 99 us (115 us)
-//   32 requests, 64 nodes, 64 / 8 heads: 155 GFLOP, 94 us; 190 to 203 us
-//     (214 us).  A tile costs a stream 2230 cycles of softmax (two warps share
+//   4 requests of 32768 positions, 32 nodes: 540 MB, 82 us; 100 us (115 us)
+//   32 requests, 64 nodes, 64 / 8 heads: 155 GFLOP, 94 us; 192 to 200 us
+//     (210 us).  A tile costs a stream 2230 cycles of softmax (two warps share
 //     a quarter's exponentials), 1024 of products and 600 of hand-over; the two
 //     streams keep the tensor cores at 40 %, the exponentials at 41 %
 //   one request, 700 positions, 8 nodes: 12.4 us; start-up, one cold pass
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The line of units: request, KV head, row-tile pair, tile.  When all
   // requests have the same number of pairs the pair comes first: the CTAs
   // that need the same keys and values are then at them at the same time, and
-  // all but one find them in L2 (512 rows per KV head, 32 requests: 370
+  // all but one find them in L2 (512 rows per KV head, 32 requests: 352
   // instead of 659 MB from memory)
   const int levels = uniform ? a.pairs : 1;
   int level = 0, in_level = u_begin;
