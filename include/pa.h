@@ -485,8 +485,10 @@ int pa_norm_rope_and_cache(pa_bf16* q_out, int64_t q_out_stride, pa_bf16* k_out,
  *
  * A node that attends to nothing, and every row t >= n, gets out = 0.
  * What lies at positions that a node does not attend to has no effect on it,
- * infinities and NaN included.  fp32 online softmax; probabilities are
- * rounded to bf16 for the tensor-core product, as in pa_decode.
+ * infinities and NaN included.  A value that is not finite under an attended
+ * position leaves its element of the row not finite, however small the
+ * weight.  fp32 online softmax; probabilities are rounded to bf16 for the
+ * tensor-core product, as in pa_decode.
  *
  * q, out     : bf16 [batch][num_nodes][num_q_heads][head_dim]; out in device
  *              or pinned host memory as for pa_decode, not overlapping q

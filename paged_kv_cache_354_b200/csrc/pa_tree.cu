@@ -262,6 +262,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 2^x, x <= 0, as the weight of a stream or a partial that is joined with
+// others: never 0, since a value that is not finite keeps its effect however
+// small the weight is
+__device__ __forceinline__ float weight_of(float x) { return fmaxf(ex2(x), 0x1p-149f); }
+
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float m;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
@@ -1060,6 +1065,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc::fence_after_sync();
       float keep0 = 1.f, keep1 = 0.f;  // factors of the own and the other stream's O
+      const bool none0 = m == -INFINITY && l == 0.f;  // the stream saw nothing of the row
+      bool none1 = true;
       if (!two) {
         xch[s * kRows + row] = make_float2(m, l);
         mbar_arrive(xch_full(s));
@@ -1067,9 +1074,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ++xch_phase;
         const float2 o = xch[(s ^ 1) * kRows + row];
+        none1 = o.x == -INFINITY && o.y == 0.f;
         const float mn = fmaxf(m, o.x);
-        keep0 = m == -INFINITY ? 0.f : ex2(m - mn);
-        keep1 = o.x == -INFINITY ? 0.f : ex2(o.x - mn);
+        keep0 = weight_of(m - mn);
+        keep1 = weight_of(o.x - mn);
         l = l * keep0 + o.y * keep1;
         m = mn;
       }
@@ -1083,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           keep1 *= inv;
         }
         // an accumulator whose stream saw nothing of the row may hold anything
-        const bool bare = __any_sync(kFull, keep0 == 0.f || (!two && keep1 == 0.f));
+        const bool bare = __any_sync(kFull, none0 || (!two && none1));
         const int64_t out_row = (static_cast<int64_t>(b) * a.nodes + token) * a.num_q_heads + h * a.group + row_head;
         const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + segs[j].slot;
         const int part_row = rt * kRows + row;
@@ -1102,8 +1110,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (bare) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              own[e] = keep0 == 0.f ? 0u : own[e];
-              other[e] = keep1 == 0.f ? 0u : other[e];
+              own[e] = none0 ? 0u : own[e];
+              other[e] = none1 ? 0u : other[e];
             }
           }
           float o[32];
@@ -1184,10 +1192,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // 33 MB, 16 us cold, 12 us of a call), else its start: 4 us of a call.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeBatch = 4;  // partials in flight
-
-// 2^x, x <= 0, as a partial's weight: never 0, since an infinite value keeps
-// its effect however small the weight is
-__device__ __forceinline__ float weight_of(float x) { return fmaxf(ex2(x), 0x1p-149f); }
 
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeArgs a, int launched) {

@@ -437,3 +437,57 @@ def test_full_size_heads(workload, nodes):
     rng = np.random.default_rng(20)
     lens = rng.integers(512, 4096, 3)
     Case(lens, None, nodes, s.num_q_heads, s.num_kv_heads, s.head_dim, s.block_size, seed=21).check()
+
+
+@pytest.mark.parametrize("nodes,hq,d,tiles", [(8, 8, 128, 2), (8, 8, 64, 2), (8, 8, 128, 3), (60, 8, 128, 2), (60, 8, 64, 3)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_a_value_that_is_not_finite_in_an_outweighed_prefix_position(nodes, hq, d, tiles, value):
+    """Every node attends to the prefix, so a value there that is not finite
+    shows in its column of every row, however little its weight: in each tile,
+    with the dominating key in each other one.  As many equal items per CTA, of
+    one row tile (8 nodes) or of two (60), so that none of them is cut."""
+    hkv = 2
+    batch = torch.cuda.get_device_properties(0).multi_processor_count
+    length = 128 * tiles
+    c = Case([length] * batch, None, nodes, hq, hkv, d, 16, seed=60, scale=1.0)
+    c.q.fill_(2.0)
+    last = length - nodes - 1
+    where = [5, 131, 260][:tiles]
+    pairs = [(i, j) for i in range(tiles) for j in range(tiles) if i != j]  # value's tile, key's tile
+    for b in range(batch):
+        block, off = c.slot(b, where[pairs[b % len(pairs)][1]])
+        c.pool[block, 0, :, off] = 4.0  # a logit of 8 d; the others are within a few times 2 sqrt(d)
+    clean = c.run()
+    assert torch.isfinite(clean).all() and max(where) < last
+    for b in range(batch):
+        block, off = c.slot(b, where[pairs[b % len(pairs)][0]] + 1)
+        c.pool[block, 1, :, off, 7] = value
+    got = c.run()
+    hit = got[..., 7]
+    assert torch.isnan(hit).all() if math.isnan(value) else not torch.isfinite(hit).any()
+    got[..., 7] = clean[..., 7]
+    assert torch.equal(got, clean)
+    assert pk.pa_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_such_a_value_in_a_request_that_is_cut(d, value):
+    """The same in one long request, a few tiles per CTA: join and merge."""
+    nodes, length = 8, 60000
+    c = Case([length], None, nodes, 8, 1, d, 16, seed=61, scale=1.0)
+    c.q.fill_(2.0)
+    block, off = c.slot(0, 128 * 7 + 3)
+    c.pool[block, 0, :, off] = 4.0
+    clean = c.run()
+    for tile in (0, 1, 4, 5, 6, 7, 8, 9, 300, 301):
+        block, off = c.slot(0, 128 * tile + 50)
+        was = c.pool[block, 1, 0, off, 9].clone()
+        c.pool[block, 1, 0, off, 9] = value
+        got = c.run()
+        c.pool[block, 1, 0, off, 9] = was
+        hit = got[..., 9]
+        assert torch.isnan(hit).all() if math.isnan(value) else not torch.isfinite(hit).any(), tile
+        got[..., 9] = clean[..., 9]
+        assert torch.equal(got, clean)
+    assert pk.pa_device_error() == 0
