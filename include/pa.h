@@ -500,9 +500,10 @@ int pa_norm_rope_and_cache(pa_bf16* q_out, int64_t q_out_stride, pa_bf16* k_out,
  *              One outside [0, min(num_nodes, L)] flags PA_DEVERR_TREE and
  *              the request's out is 0 (a request with L = 0 is empty and
  *              never flagged for that).
- * Other arguments, length and block checks as pa_decode; seq_lens include
- * the nodes.  num_nodes 1..1024, head_dim in {64, 128}, block_size in
- * {16, 32}, num_q_heads / num_kv_heads 1..64, batch <= 32768.
+ * Other arguments, length and block checks as pa_decode; scale times log2(e)
+ * has to be finite too; seq_lens include the nodes.  num_nodes 1..1024,
+ * head_dim in {64, 128}, block_size in {16, 32}, num_q_heads / num_kv_heads
+ * 1..64, batch <= 32768.
  * workspace from pa_decode_tree_workspace_size (256-byte aligned, no
  * initialisation; calls that can overlap need one each).
  * ------------------------------------------------------------------------ */

@@ -1371,6 +1371,9 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   int rc = check_tree_shape(who, batch, num_nodes, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len);
   if (rc != PA_OK) return rc;
   if (num_blocks <= 0 || max_blocks_per_seq <= 0) return fail(PA_ERR_INVALID, "%s: non-positive size", who);
+  // smallest normal for 0: masked logits stay -inf, the others vanish
+  const float scale_log2 = scale == 0.f ? FLT_MIN : fabsf(scale) * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return fail(PA_ERR_INVALID, "%s: scale is not finite, or not times log2(e)", who);
   if (batch == 0) return PA_OK;
   if (!out || !q || !kv_pool || !tree_mask || !block_tables || !seq_lens || !workspace)
     return fail(PA_ERR_INVALID, "%s: NULL pointer", who);
@@ -1408,8 +1411,7 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   a.num_blocks = num_blocks;
   a.max_blocks = max_blocks_per_seq;
   a.max_seq_len = std::min(max_seq_len, 0x7fffffff - 4096);  // positions of a tile stay in range
-  // smallest normal for 0: masked logits stay -inf, the others vanish
-  a.scale_log2 = scale == 0.f ? FLT_MIN : fabsf(scale) * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.negative = scale < 0.f;
   a.tile_tokens = std::min(kRows / a.group, num_nodes);
   a.pairs = (num_nodes + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);

@@ -131,3 +131,11 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         pk.pa_decode_tree(q, q, q, i, i, i, 1, 1.0, i)
     with pytest.raises(TypeError, match="CUDA"):
         pk.pa_tree_accept(q, i, i, i, i, i)
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf"), 3.4e38, -3.4e38])
+def test_decode_tree_refuses_a_scale_that_is_not_finite(scale):
+    """... or whose product with log2(e) is not."""
+    assert lib.pa_decode_tree(A, 2 * A, A, A, 1, A, A, None, 2, 3, 8, 2, 128, 16, 10, 4, 64, scale, A, 1 << 40,
+                              None) == pk.PA_ERR_INVALID
+    assert "scale" in message()
