@@ -447,6 +447,9 @@ int pa_plan_append(int32_t* block_tables, const int32_t* blocks_held, int32_t* f
  *                8: slices of a fused projection's output need no copy.
  * q_out        : device bf16 at q_out_stride; may be q itself (same stride).
  * k_out        : device bf16 at k_out_stride, may be k itself; or NULL.
+ *                Apart from these two cases no output (q_out, k_out, the pool)
+ *                shares memory with q, k, v or another output; tokens' rows
+ *                may lie between one another's.
  * kv_pool      : device bf16 pool (layout above); NULL: nothing is cached (v
  *                and slot_mapping are not read).
  * q_weight, k_weight : device bf16 [head_dim] or NULL.

@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <numeric>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -215,6 +216,25 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) norm_rope_kernel(co
   }
 }
 
+// `count` rows of `row` bytes, `stride` bytes apart; count 0: not used.
+struct Rows {
+  const void* at;
+  int64_t count, stride, row;
+};
+
+// Whether two of them share a byte.  Exact for equal strides, where rows meet
+// when they meet modulo the stride; of different ones the greatest common
+// divisor takes that place, and rows may be taken to meet that do not.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.count == 0 || b.count == 0) return false;
+  const int64_t from = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.at) - reinterpret_cast<uintptr_t>(a.at));
+  if (from >= (a.count - 1) * a.stride + a.row || -from >= (b.count - 1) * b.stride + b.row) return false;
+  const int64_t g = std::gcd(a.count > 1 ? a.stride : 0, b.count > 1 ? b.stride : 0);
+  if (g == 0) return true;
+  const int64_t at = (from % g + g) % g;
+  return at < a.row || g - at < b.row;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -263,6 +283,16 @@ extern "C" int pa_norm_rope_and_cache(pa_bf16* q_out, int64_t q_out_stride, pa_b
                   static_cast<long long>(s.stride), static_cast<long long>(s.row));
   if ((q_out == q && q_out_stride != q_stride && num_q_heads > 0) || (k_out && k_out == k && k_out_stride != k_stride))
     return fail(PA_ERR_INVALID, "%s: in place needs equal strides", who);
+  // another group of lanes reads what an output over its input overwrites
+  const int64_t qn = num_q_heads > 0 ? num_tokens : 0, kn = num_kv_heads > 0 ? num_tokens : 0;
+  const Rows in_q{q, qn, 2 * q_stride, 2 * q_row}, in_k{k, kn, 2 * k_stride, 2 * k_row},
+      in_v{v, kv_pool ? kn : 0, 2 * v_stride, 2 * k_row}, to_q{q_out, qn, 2 * q_out_stride, 2 * q_row},
+      to_k{k_out, k_out ? kn : 0, 2 * k_out_stride, 2 * k_row},
+      to_pool{kv_pool, kv_pool && kn ? 1 : 0, 0, 4 * k_row * num_blocks * block_size};
+  if ((q_out != q && overlap(to_q, in_q)) || overlap(to_q, in_k) || overlap(to_q, in_v) || overlap(to_k, in_q) ||
+      (k_out != k && overlap(to_k, in_k)) || overlap(to_k, in_v) || overlap(to_k, to_q) || overlap(to_pool, in_q) ||
+      overlap(to_pool, in_k) || overlap(to_pool, in_v) || overlap(to_pool, to_q) || overlap(to_pool, to_k))
+    return fail(PA_ERR_INVALID, "%s: an output overlaps an input or another output", who);
   int32_t* err = device_error_word();
   if (err == nullptr) return PA_ERR_CUDA;
   RopeArgs a;

@@ -212,3 +212,43 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         check(outs[i], pools[i], None, q, k, v, slots, pos, weights, cs, False)
+
+
+def test_outputs_between_the_inputs_of_one_slab():
+    """Results beside their inputs in one slab, in place, and one token
+    directly behind the other: nothing is shared, so nothing is refused."""
+    n, hq, hkv, d = 21, 4, 2, 64
+    rng = np.random.default_rng(14)
+    pool = torch.full((4, 2, hkv, 16, d), 7.5, dtype=torch.bfloat16, device="cuda")
+    weights = [(1 + 0.2 * workloads.bf16_normal((d,), seed=i)).bfloat16().cuda() for i in range(2)]
+    slots, pos = rng.permutation(64)[:n], rng.integers(0, 500, n)
+    cs = table(500, d).cuda()
+    heads = (hq, hkv, hkv, hq, hkv)  # q, k, v, q_out, k_out
+    slab = workloads.bf16_normal((n, sum(heads) * d), seed=15).cuda()
+    q, k, v, q_out, k_out = (x.unflatten(1, (-1, d)) for x in slab.split([h * d for h in heads], 1))
+    was = q.clone(), k.clone(), v.clone()
+    g_slots, g_pos = torch.as_tensor(slots).cuda(), torch.as_tensor(pos).int().cuda()
+    pk.pa_norm_rope_and_cache(q_out, q, k, v, pool, g_slots, g_pos, cs, *weights, eps=EPS, k_out=k_out)
+    check(q_out, pool, k_out, *was, slots, pos, weights, cs, False)
+    assert all(torch.equal(x, w) for x, w in zip((q, k, v), was))
+    pool.fill_(7.5)
+    pk.pa_norm_rope_and_cache(q, q, k, v, pool, g_slots, g_pos, cs, *weights, eps=EPS, k_out=k)
+    check(q, pool, k, *was, slots, pos, weights, cs, False)
+    # contiguous tensors one behind the other in a single buffer
+    sizes = [n * h * d for h in (hq, hkv, hkv, hq, hkv)] + [pool.numel()]
+    flat = workloads.bf16_normal((sum(sizes),), seed=16).cuda()
+    parts = flat.split(sizes)
+    q, k, v, q_out, k_out = (x.view(n, -1, d) for x in parts[:5])
+    pool = parts[5].view(pool.shape).fill_(7.5)
+    was = q.clone(), k.clone(), v.clone()
+    pk.pa_norm_rope_and_cache(q_out, q, k, v, pool, g_slots, g_pos, cs, *weights, eps=EPS, k_out=k_out)
+    check(q_out, pool, k_out, *was, slots, pos, weights, cs, False)
+    assert all(torch.equal(x, w) for x, w in zip((q, k, v), was))
+
+
+def test_an_output_over_another_tokens_input_is_refused():
+    q, k, v, pool, slots, pos, weights = make(12, 4, 2, 64, 16, 17)
+    buffer = torch.zeros((13, 4, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(pk.PaError, match="overlap"):
+        pk.pa_norm_rope_and_cache(buffer[1:], buffer[:-1], k, v, pool, torch.as_tensor(slots).cuda(),
+                                  torch.as_tensor(pos).int().cuda(), table(500, 64).cuda(), *weights, eps=EPS)

@@ -139,3 +139,30 @@ def test_decode_tree_refuses_a_scale_that_is_not_finite(scale):
     assert lib.pa_decode_tree(A, 2 * A, A, A, 1, A, A, None, 2, 3, 8, 2, 128, 16, 10, 4, 64, scale, A, 1 << 40,
                               None) == pk.PA_ERR_INVALID
     assert "scale" in message()
+
+
+def test_norm_rope_refuses_outputs_over_inputs_and_one_another():
+    """Token rows that share memory, at any offset, are refused unless an
+    output lies exactly over its own input.  Three tokens of 4 and 2 heads of
+    64; every tensor is far from the others unless the case says so."""
+    far = {name: A << i for i, name in enumerate(("q", "k", "v", "q_out", "pool"), 1)}
+    q, k, v, pool = (far[n] for n in ("q", "k", "v", "pool"))
+    q_bytes, k_bytes = 3 * 512, 3 * 256
+    pool_bytes = 4 * 2 * 2 * 16 * 64 * 2
+    bad = [
+        {"q_out": q + 16}, {"q_out": q + q_bytes - 16}, {"q_out": q - 16}, {"q_out": q - q_bytes + 16},
+        {"q_out": k}, {"q_out": k + k_bytes - 16}, {"q_out": k - q_bytes + 16}, {"q_out": v}, {"q_out": v + 16},
+        {"k_out": q, "kos": 128}, {"k_out": q + 16, "kos": 128}, {"k_out": k + 16, "kos": 128},
+        {"k_out": v, "kos": 128}, {"k_out": far["q_out"] + 32, "kos": 128}, {"k_out": pool, "kos": 128},
+        {"q_out": pool + pool_bytes - 16}, {"q": pool}, {"k": pool + 64}, {"v": pool + pool_bytes - 16},
+        {"k": q, "q_out": q},  # in place, and the keys read there too
+        {"v": k, "k_out": k, "kos": 128},
+        # slices of one slab of 8 heads a token: the queries' result over the last head of the queries
+        {"q": q, "qs": 512, "q_out": q + 3 * 128, "qos": 512},
+        {"q": q, "qs": 512, "k": q + 512, "ks": 512, "q_out": q + 3 * 128, "qos": 512},
+        {"k": q + 512, "ks": 512, "q": q, "qs": 512, "k_out": q + 128, "kos": 512},
+        {"q": q, "qs": 512, "q_out": q + 1024 - 16, "qos": 512},  # its end over the next token
+        {"q": q, "qs": 512, "q_out": q + 512, "qos": 256},  # strides apart
+    ]
+    for more in bad:
+        assert rope(**(far | more)) == pk.PA_ERR_INVALID and "overlap" in message(), more
