@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fetch = [&](const Item& it, int tile) -> int {
       const unsigned e = static_cast<unsigned>(tile) * G::kTileBlocks + lane;
       return e * BS < static_cast<unsigned>(it.len)
-                 ? __ldg(a.block_tables + static_cast<int64_t>(it.b) * a.max_blocks + e)
+                 ? a.block_tables[static_cast<int64_t>(it.b) * a.max_blocks + e]
                  : 0;
     };
     Item cur{0, 0, 0, 0, 0, 0, 0};
