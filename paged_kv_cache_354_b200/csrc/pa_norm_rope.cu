@@ -73,7 +73,9 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) norm_rope_kernel(const RopeArgs a) {
   constexpr int kLanes = D / 16;  // per row
-  pdl_trigger();
+  // the cache write and the fused append read new keys through the read-only
+  // path: they must not be resident while k_out is written
+  if (a.k_out == nullptr) pdl_trigger();
   pdl_wait();
   const int l = threadIdx.x & (kLanes - 1);
   // the two chunks of this lane

@@ -18,6 +18,11 @@
 // any barrier.  Bytes bound it when there are many rows: kAcceptBatch steps of
 // a thread are in flight at once, and 600 paths of up to 16 rows of 4 KB (39
 // MB) move in 8.5 us, 4.6 TB/s; 64 paths of up to 6 take 2.8 us.
+//
+// Neither lets the next kernel start early.  The decodes and the cache write
+// read tables, lengths and slots through the read-only path, so they must not
+// be resident while these are written.  That costs nothing: a captured step of
+// 4 trees of 8 takes 24.3 us (26.4 with early starts), of 64 of 16 126 us (126).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -147,7 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_append_kernel(const PlanArg
   };
   int rank = 0;
   if constexpr (kRanks > 1) rank = static_cast<int>(cg::this_cluster().block_rank());
-  pdl_trigger();
+  if (!kSlots && a.num_slots > 0) pdl_trigger();  // for the slots kernel, which waits
   pdl_wait();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   // this thread's requests, a run of them; few requests are spread over all
@@ -306,7 +311,6 @@ constexpr int kSlotThreads = 256;
 
 __global__ void __launch_bounds__(kSlotThreads) plan_slots_kernel(const PlanArgs a) {
   __shared__ int starts[kSlotThreads + 1];
-  pdl_trigger();
   pdl_wait();
   const int t = threadIdx.x, lane = t & 31;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSlotThreads, i = i0 + t;
@@ -376,7 +380,6 @@ struct AcceptArgs {
 __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const AcceptArgs a) {
   extern __shared__ int64_t rows[];  // [max_path] source, [max_path] target: element offset of the key row of head 0
   __shared__ int bad;
-  pdl_trigger();
   if (threadIdx.x == 0) bad = 0;
   pdl_wait();
   __syncthreads();

@@ -22,3 +22,14 @@ def test_tree_calls_read_what_a_step_writes_with_ordinary_loads():
         text = source(name)
         assert [x for x in re.findall(r"__ldg\(([^;]*);", text) if "weight" not in x] == []
         assert "ld.global.nc" not in text and "__restrict__" not in text
+
+
+def test_what_the_read_only_path_reads_is_written_before_its_reader_starts():
+    """The decodes and the cache write take tables, lengths, slots and new keys
+    through the read-only path.  A kernel that writes one of them does not let
+    the next one start early, unless that one is its own call's second kernel
+    (a large plan's slots) or nothing of the kind is written (no k_out)."""
+    assert [line.split("//")[0].strip() for line in source("pa_plan.cu").splitlines() if "pdl_trigger" in line] == [
+        "if (!kSlots && a.num_slots > 0) pdl_trigger();"]
+    assert [line.strip() for line in source("pa_norm_rope.cu").splitlines() if "pdl_trigger" in line] == [
+        "if (a.k_out == nullptr) pdl_trigger();"]
