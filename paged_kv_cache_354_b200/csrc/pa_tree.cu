@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // that need the same keys and values are then at them at the same time, and
   // all but one find them in L2 (512 rows per KV head, 32 requests: 352
   // instead of 659 MB from memory)
-  const int levels = uniform ? a.pairs : 1;
+  const int levels = uniform && total > 0 ? a.pairs : 1;
   int level = 0, in_level = u_begin;
   if (levels > 1) {
     level = u_begin / (total / levels);

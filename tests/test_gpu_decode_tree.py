@@ -491,3 +491,10 @@ def test_such_a_value_in_a_request_that_is_cut(d, value):
         got[..., 9] = clean[..., 9]
         assert torch.equal(got, clean)
     assert pk.pa_device_error() == 0
+
+
+@pytest.mark.parametrize("lens,counts", [([0, 0, 0], None), ([0, 0], [0, 0]), ([50, 0, 700], [0, 0, 0])])
+def test_no_request_has_a_node(lens, counts):
+    """Nothing to do at sizes of several row-tile pairs: all rows are zeroed."""
+    out = Case(lens, counts, 300, 4, 2, 128, 16, seed=62).run()
+    assert not out.any() and pk.pa_device_error() == 0
