@@ -498,3 +498,21 @@ def test_no_request_has_a_node(lens, counts):
     """Nothing to do at sizes of several row-tile pairs: all rows are zeroed."""
     out = Case(lens, counts, 300, 4, 2, 128, 16, seed=62).run()
     assert not out.any() and pk.pa_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs", [(16, 4, 128, 16), (4, 4, 64, 32), (32, 2, 128, 16)])
+def test_one_node_matches_single_token_pa_decode(hq, hkv, d, bs):
+    """A tree of one node is the newest token: both answers lie within the
+    roundings of the exact one that each call makes."""
+    lens = [1, 5, 300, 1200, 64, 129]
+    c = Case(lens, None, 1, hq, hkv, d, bs, seed=63)
+    got = c.run().float()
+    need, _ = pk.pa_decode_workspace_size(len(lens), hq, hkv, d, bs, 1200)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+    single = torch.empty((len(lens), hq, d), dtype=torch.bfloat16, device="cuda")
+    pk.pa_decode(single, c.q[:, 0].contiguous().cuda(), c.pool.cuda(), torch.as_tensor(c.tables).cuda(),
+                 torch.as_tensor(c.lens).cuda(), 1200, c.scale, workspace=ws)
+    want, spread, size, logit = c.want()
+    both = torch.as_tensor(2 * c.tolerance(want, spread, size, logit)).cuda()
+    assert ((got - single.float()[:, None]).abs() <= both).all()
+    c.check(got.bfloat16())

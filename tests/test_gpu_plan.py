@@ -255,3 +255,27 @@ def test_refused_large_calls_change_nothing(what, packed):
     for t, was in zip((s.g_tables, s.g_held, s.g_free, s.g_num, s.g_lens), before):
         assert torch.equal(t, was)
     assert (slots == -1).all() and (positions == -1).all() and (starts == 0).all()
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("batch,most", [(700, 12), (2500, 3)])
+def test_depths_in_large_plans(batch, most, shared):
+    """Tree positions where several CTAs share the requests, some of which end,
+    the state in place and then apart."""
+    rng = np.random.default_rng(batch)
+    s = State(rng, batch, 16, 8, 60, batch * 3)
+    for apart in (False, True):
+        new = [int(x) if rng.random() > 0.1 else -1 for x in rng.integers(0, most, batch, endpoint=True)]
+        depth = rng.integers(0, 40, (most,) if shared else (batch, most))
+        at = np.broadcast_to(depth, (batch, most))
+        lens, want = list(s.lens), s.want(new)
+        out = [torch.full_like(t, -5) for t in (s.g_lens, s.g_held, s.g_num)] if apart else None
+        slots, positions, _ = call(s, new, most, depths=dev(depth), out=out)
+        assert slots.tolist() == [x + [-1] * (most - len(x)) for x in want[4]]
+        assert positions.tolist() == [[lens[b] + int(at[b, t]) if t < new[b] else -1 for t in range(most)]
+                                      for b in range(batch)]
+        if apart:
+            s.g_lens, s.g_held, s.g_num = out
+        s.same(want)
+        s.tables, s.held, s.free, s.lens = want[:4]
+    assert pk.pa_device_error() == 0
