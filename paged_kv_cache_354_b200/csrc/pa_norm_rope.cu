@@ -16,7 +16,7 @@
 // 16384 tokens of 32 + 8 + 8 heads of 128 (411 MB): 78 us = 5.3 TB/s, 80 % of
 // a copy.  Without resident blocks it took 96 us, with 4 rows and 6 blocks per
 // SM 88 us (spills), with 8 rows and 3 blocks 92 us, with streaming loads 80
-// us.  1024 tokens (25.7 MB): 6.2 us.
+// us.  1024 tokens (25.7 MB): 6.4 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -6,18 +6,18 @@
 // handed out is entry F + R - 1 - k of the free stack (F free before, R given
 // back), so no request waits for another one's pop.  Latency is all the cost:
 // a decoding step is one CTA, and its barriers and dependent loads take the
-// time (64 requests of 16 tokens: 5.3 us, 15 KB).  From kPlanSpread slots or
+// time (64 requests of 16 tokens: 5.2 us, 15 KB).  From kPlanSpread slots or
 // kPlanMany requests on a cluster of 8 shares the requests and exchanges its
 // sums through distributed shared memory, and a packed call of that size
 // leaves its slots to a second, wide launch (1000 requests, 256k slots: 328 us
-// on one CTA, 66 us when the cluster wrote the slots, 14.4 us so; floor 0.6 us).
+// on one CTA, 66 us when the cluster wrote the slots, 13.2 us so; floor 0.6 us).
 //
 // pa_tree_accept moves rows of the pool.  A thread owns one 16-byte column of
 // the rows of one request and walks the path in order: step i writes row i
 // and reads row path[i] >= i, so no row is written before it is read, without
 // any barrier.  Bytes bound it when there are many rows: kAcceptBatch steps of
 // a thread are in flight at once, and 600 paths of up to 16 rows of 4 KB (39
-// MB) move in 8.5 us, 4.6 TB/s; 64 paths of up to 6 take 2.8 us.
+// MB) move in 8.4 us, 4.6 TB/s; 64 paths of up to 6 take 2.6 us.
 //
 // Neither lets the next kernel start early.  The decodes and the cache write
 // read tables, lengths and slots through the read-only path, so they must not
@@ -97,8 +97,8 @@ __device__ __forceinline__ long long warp_inclusive(long long v, int lane) {
 // Every lane's run of `count` entries, from src on upwards (dir 1) or downwards
 // (-1), to dst on: eight lanes to a run, four runs at a time, kRunDepth entries
 // per lane in flight.  (A warp to a run waits for memory once per run: the
-// whole call 16.8 us instead of 14.4 in the case above; all runs in one line,
-// each lane looking up the owner of its entries, 15.9.)
+// whole call 16.8 us where this took 14.4 in the case above; all runs in one
+// line, each lane looking up the owner of its entries, 15.9.)
 constexpr int kRunDepth = 8;
 
 __device__ __forceinline__ void copy_runs(int count, const int32_t* src, int dir, int32_t* dst, int lane) {
@@ -490,6 +490,10 @@ int pa_plan_append(int32_t* block_tables, const int32_t* blocks_held, int32_t* f
     PA_CUDA_TRY(launch_pdl(plan_append_kernel<1, true>, dim3(1), dim3(kPlanThreads), 0, st, a));
     return PA_OK;
   }
+  // Padded slots need no search for their request, and the cluster writes them
+  // with the sums at hand: 16,000 slots of 1000 requests in 8.8 us (packed, with
+  // the second launch, 10.0), 32,000 of 2000 in 10.9 (10.1).  Beyond that eight
+  // CTAs are too few: 128,000 of 2000 take 21.5 (10.9).
   const bool wide = max_new_tokens == 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kPlanCluster);

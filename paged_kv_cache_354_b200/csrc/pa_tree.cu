@@ -33,13 +33,15 @@
 // Bounds and what it takes (times of the GPU alone; in long runs the power
 // limit lowers the clock and adds the second figure):
 //   64 requests of about 2250 positions, 16 nodes, 32 / 8 heads of 128: 625 MB,
-//     95 us at copy rate; 111 us = 5.6 TB/s (129 us).  Memory, and per item
+//     95 us at copy rate; 110 us = 5.7 TB/s (120 to 132 us).  Memory, and per item
 //     some 8000 cycles in which both streams end one item and begin the next
-//   4 requests of 32768 positions, 32 nodes: 540 MB, 82 us; 100 us (115 us)
-//   32 requests, 64 nodes, 64 / 8 heads: 155 GFLOP, 94 us; 192 to 200 us
-//     (210 us).  A tile costs a stream 2230 cycles of softmax (two warps share
-//     a quarter's exponentials), 1024 of products and 600 of hand-over; the two
-//     streams keep the tensor cores at 40 %, the exponentials at 41 %
+//   4 requests of 32768 positions, 32 nodes: 540 MB, 82 us; 98 to 100 us (109
+//     to 115 us)
+//   32 requests, 64 nodes, 64 / 8 heads: 155 GFLOP, 94 us; 192 to 200 us (207
+//     to 212 us).  A tile costs a stream 2230 cycles of softmax (two warps share
+//     a quarter's exponentials), 1024 of products and 600 of hand-over (clock
+//     stamps in a copy of the kernel); the two streams keep the tensor cores at
+//     40 %, the exponentials at 41 %
 //   one request, 700 positions, 8 nodes: 12.4 us; start-up, one cold pass
 //     through the code, the merge (4 us)
 //
@@ -1417,8 +1419,10 @@ int pa_decode_tree(pa_bf16* out, const pa_bf16* q, const pa_bf16* kv_pool, const
   a.pairs = (num_nodes + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
   // exact: the factor is above 2^20 / d by less than 1, x d <= 1279 * 256 < 2^20
   a.pair_factor = ((1 << 20) + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
-  // ending one item and beginning the next takes as long as some tiles (64
-  // trees of 16: 111.2 us with 3, 111.6 with 2, 112.3 with 4, 116.5 with 8)
+  // ending one item and beginning the next takes as long as some tiles.  With
+  // 1, 2, 3, 4, 6: 64 trees of 16 116.0, 110.4, 109.8, 111.1, 112.9 us; 512 rows
+  // per KV head 195.7, 195.2, 194.0, 194.6, 196.4; ragged short requests at head
+  // dim 64 27.6, 25.6, 25.8, 26.5, 27.3; long contexts 97.8 to 98.8 with any
   a.extra = 3;
   const unsigned ctas = std::max(sm_count(), 1);
   a.cta_factor = ctas > 1 ? 0xffffffffu / ctas + 1 : 0;  // exact: x ctas < ctas^3 < 2^32
